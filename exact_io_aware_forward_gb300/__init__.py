@@ -15,6 +15,8 @@ from .api import (FAError, backward, fa_backward, fa_backward_dkdv, fa_backward_
                   fa_backward_dk_dv_dropout, fa_backward_dq_dropout,
                   fa_forward_varlen, fa_backward_varlen, fa_backward_varlen_workspace_size, forward_varlen,
                   backward_varlen, fa_backward_dkdv_varlen, fa_backward_dk_dv_varlen, fa_backward_dq_varlen,
+                  PagedCache, fa_paged_append, fa_forward_paged, fa_paged_workspace_size, forward_paged,
+                  fa_paged_evict, fa_paged_evict_workspace_size,
                   fa_selftest_wait_timeout,
                   fa_backward_preprocess, fa_backward_workspace_size, fa_device_status, fa_forward,
                   fa_score_blocks, forward)

@@ -19,6 +19,15 @@ _F = ctypes.c_float
 _S = ctypes.c_size_t
 _U64 = ctypes.c_uint64
 _U32 = ctypes.c_uint32
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """fa_paged_cache."""
+    _fields_ = [("k_pages", _P), ("v_pages", _P), ("k_scale", _P), ("v_scale", _P), ("page_table", _P),
+                ("num_pages", _I), ("pages_per_seq", _I), ("B", _I), ("Hkv", _I), ("page_size", _I), ("d", _I),
+                ("cache_dtype", _I)]
+
+
 SIGNATURES = {
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_forward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
@@ -61,6 +70,11 @@ SIGNATURES = {
     "fa_backward_dk_dv_varlen": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                       _F, _P]),
     "fa_backward_dq_varlen": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
+    "fa_paged_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P]),
+    "fa_paged_workspace_size": (_S, [_P, _I, _I, _I, _I, _I]),
+    "fa_forward_paged": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _I, _P, _S, _P]),
+    "fa_paged_evict_workspace_size": (_S, [_P, _I]),
+    "fa_paged_evict": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _S, _P]),
     "fa_selftest_wait_timeout": (_I, [_P]),
     "fa_device_status": (_I, [_P]),
     "fa_score_blocks": (_I, [_P, ctypes.POINTER(_U64), ctypes.POINTER(_U64), _I]),

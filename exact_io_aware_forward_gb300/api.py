@@ -14,7 +14,7 @@ import math
 
 import torch
 
-from ._lib import lib, status_string
+from ._lib import PagedCacheStruct, lib, status_string
 
 FA_FP16, FA_BF16 = 0, 1
 _DTYPE_CODE = {torch.float16: FA_FP16, torch.bfloat16: FA_BF16}
@@ -473,6 +473,119 @@ def fa_forward_decode_gqa(q, k, v, o, lse, workspace, causal=False, scale=None, 
         workspace.data_ptr(), workspace.numel(), _stream(stream)))
 
 
+# ---------------------------------------------------------------- 8-bit paged cache
+_CACHE_CODE = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+class PagedCache:
+    """The 8-bit paged K / V cache: k_pages, v_pages [P, Hkv, page_size, d]
+    (float8_e4m3fn or float8_e5m2), k_scale, v_scale [P, Hkv] float32 and
+    page_table [B, pages_per_seq] int32, all contiguous on one CUDA device.
+    Checks them once and keeps them; the calls below take it with the
+    sequences' lengths."""
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale, page_table):
+        if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or k_pages.dtype not in _CACHE_CODE:
+            raise TypeError("k_pages must be a float8_e4m3fn or float8_e5m2 tensor [P, Hkv, page_size, d]")
+        P, Hkv, ps, d = k_pages.shape
+        ptr = [_bhnd("k_pages", k_pages), _bhnd("v_pages", v_pages, k_pages.shape, k_pages.dtype),
+               _bhnd("k_scale", k_scale, (P, Hkv), torch.float32), _bhnd("v_scale", v_scale, (P, Hkv), torch.float32),
+               _bhnd("page_table", page_table, None, torch.int32)]
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [B, pages_per_seq]")
+        self.tensors = (k_pages, v_pages, k_scale, v_scale, page_table)
+        self.device = k_pages.device
+        if any(t.device != self.device for t in self.tensors):
+            raise ValueError("the cache's tensors must be on one device")
+        self.B, self.pages_per_seq = page_table.shape
+        self.num_pages, self.Hkv, self.page_size, self.d = P, Hkv, ps, d
+        self.slots = self.pages_per_seq * ps  # a sequence's capacity
+        self._struct = PagedCacheStruct(*ptr, P, self.pages_per_seq, self.B, Hkv, ps, d, _CACHE_CODE[k_pages.dtype])
+        self._ref = ctypes.byref(self._struct)
+
+    def _stream(self, stream):
+        """The stream to launch on (current device's by default), with the cache's device current."""
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {self.device}: make it the current device")
+        return ctypes_stream(torch.cuda.current_stream() if stream is None else stream)
+
+    def _tensor(self, name, t, shape, dtype):
+        """The pointer of a contiguous tensor on the cache's device."""
+        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {tuple(shape)} {dtype} on {self.device}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+        return t.data_ptr()
+
+    def _state(self, name, t, dtype):
+        return None if t is None else self._tensor(name, t, (self.B, self.Hkv, self.slots), dtype)
+
+
+def _workspace_args(cache, workspace):
+    if workspace.dtype != torch.uint8 or workspace.device != cache.device or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor on the cache's device")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def fa_paged_append(cache, k, v, lens, new_lens, counts=None, weight_acc=None, positions=None, first_position=None,
+                    stream=None) -> None:
+    """Append k, v [B, Hkv, N, d] (counts[b] <= N tokens of each sequence, all N by default) behind the
+    lens[b] filled slots; new_lens [B] int32 (another tensor than lens) gets the lengths after.  weight_acc
+    and positions [B, Hkv, slots] are set for the new slots: 0, and first_position[b] + i (or the slot)."""
+    if k.dim() != 4 or k.dtype not in _DTYPE_CODE:
+        raise TypeError("k must be float16 or bfloat16 [B, Hkv, N, d]")
+    N, B = k.shape[2], (cache.B,)
+    shape = (cache.B, cache.Hkv, N, cache.d)
+    i32 = torch.int32
+    _check("fa_paged_append", lib().fa_paged_append(
+        cache._ref, cache._tensor("k", k, shape, k.dtype), cache._tensor("v", v, shape, k.dtype),
+        cache._tensor("lens", lens, B, i32), None if counts is None else cache._tensor("counts", counts, B, i32),
+        cache._tensor("new_lens", new_lens, B, i32), cache._state("weight_acc", weight_acc, torch.float32),
+        cache._state("positions", positions, i32),
+        None if first_position is None else cache._tensor("first_position", first_position, B, i32), N,
+        _DTYPE_CODE[k.dtype], cache._stream(stream)))
+
+
+def fa_paged_workspace_size(cache, Hq, Nq, max_len=0, num_splits=0, weights=False) -> int:
+    return int(lib().fa_paged_workspace_size(cache._ref, int(Hq), int(Nq), int(max_len), int(num_splits),
+                                             int(bool(weights))))
+
+
+def fa_forward_paged(cache, q, lens, o, lse, workspace, causal=False, scale=None, weight_acc=None, max_len=0,
+                     num_splits=0, stream=None) -> None:
+    """Attention of q [B, Hq, Nq, d] over the lens[b] slots of each sequence (Hq a multiple of Hkv; causal:
+    the queries are the last Nq slots) into o and lse [B, Hq, Nq]; weight_acc [B, Hkv, slots] gets each
+    slot's attention weight added, summed over the query rows of its head."""
+    if q.dim() != 4 or q.dtype not in _DTYPE_CODE:
+        raise TypeError("q must be float16 or bfloat16 [B, Hq, Nq, d]")
+    dt = q.dtype
+    _, Hq, Nq, d = q.shape
+    shape = (cache.B, Hq, Nq, cache.d)
+    ws, ws_bytes = _workspace_args(cache, workspace)
+    _check("fa_forward_paged", lib().fa_forward_paged(
+        cache._ref, cache._tensor("q", q, shape, dt), cache._tensor("lens", lens, (cache.B,), torch.int32),
+        cache._tensor("o", o, shape, dt), cache._tensor("lse", lse, shape[:3], torch.float32),
+        cache._state("weight_acc", weight_acc, torch.float32), Hq, Nq, _DTYPE_CODE[dt], int(bool(causal)),
+        _scale(scale, d), int(max_len), int(num_splits), ws, ws_bytes, cache._stream(stream)))
+
+
+def fa_paged_evict_workspace_size(cache, keep) -> int:
+    return int(lib().fa_paged_evict_workspace_size(cache._ref, int(keep)))
+
+
+def fa_paged_evict(cache, lens, new_lens, weight_acc, positions, workspace, keep, recent, stream=None) -> None:
+    """Keep, per sequence and head, `keep` slots: those of the last `recent` positions, then those of largest
+    weight_acc; kept slots behind the new length move into the holes before it, with their weight_acc and
+    positions [B, Hkv, slots].  new_lens [B] int32 (another tensor than lens) gets min(lens, keep)."""
+    ws, ws_bytes = _workspace_args(cache, workspace)
+    B = (cache.B,)
+    if weight_acc is None or positions is None:
+        raise TypeError("weight_acc and positions are needed to choose what stays")
+    _check("fa_paged_evict", lib().fa_paged_evict(
+        cache._ref, cache._tensor("lens", lens, B, torch.int32), cache._tensor("new_lens", new_lens, B, torch.int32),
+        cache._state("weight_acc", weight_acc, torch.float32), cache._state("positions", positions, torch.int32),
+        int(keep), int(recent), ws, ws_bytes, cache._stream(stream)))
+
+
 def fa_selftest_wait_timeout(stream=None) -> None:
     """Enqueue the failure-detection self-test (a bounded wait that never
     completes; ~2 s); the next fa_device_status() raises FA_ERR_TIMEOUT."""
@@ -526,6 +639,20 @@ def forward_decode(q, k, v, causal=False, scale=None, num_splits=0, stream=None,
         fa_forward_decode_gqa(q, k, v, o, lse, workspace, causal, scale, num_splits, stream)
     else:
         fa_forward_decode(q, k, v, o, lse, workspace, causal, scale, num_splits, stream)
+    return o, lse
+
+
+def forward_paged(cache, q, lens, causal=False, scale=None, weight_acc=None, max_len=0, num_splits=0, stream=None,
+                  workspace=None):
+    """Return (O, LSE) of q [B, Hq, Nq, d] over the 8-bit paged cache (arguments as fa_forward_paged)."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Nq, d]")
+    if workspace is None:
+        n = fa_paged_workspace_size(cache, q.shape[1], q.shape[2], max_len, num_splits, weight_acc is not None)
+        workspace = torch.empty(max(n, 1), device=q.device, dtype=torch.uint8)
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
+    fa_forward_paged(cache, q, lens, o, lse, workspace, causal, scale, weight_acc, max_len, num_splits, stream)
     return o, lse
 
 

@@ -8,6 +8,7 @@
 #include "../../include/fa_gb300.h"
 #include "fa_decode.h"
 #include "fa_internal.h"
+#include "fa_paged.h"
 
 namespace {
 
@@ -355,6 +356,17 @@ fa_status run_backward(const Shape& s, const void* q, const void* k, const void*
 }  // namespace
 
 namespace fa {
+unsigned int* device_status_word() { return status_word(); }
+
+bool encode_tiled_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const cuuint64_t (&dims)[3],
+                      const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int backward_arguments_status(const void* q, const void* k, const void* v, const void* o, const void* dO,
                               const float* lse, const void* dq, const void* dk, const void* dv, int B, int H, int N,
                               int d, int dtype, float scale) {
@@ -382,6 +394,8 @@ const char* fa_status_string(int status) {
       return "FA_ERR_SCRATCH_TOO_SMALL: fa_backward_noalloc needs more than its fixed 32 MiB scratch; use fa_backward";
     case FA_ERR_SEQLENS:
       return "FA_ERR_SEQLENS: a cu_seqlens range exceeded the packed totals or the maximum lengths; it was skipped";
+    case FA_ERR_PAGES:
+      return "FA_ERR_PAGES: a page table entry lay outside the page pool; its slots were skipped";
     default: return "unknown fa_status";
   }
 }
@@ -764,6 +778,7 @@ fa_status fa_device_status(void* stream) {
     if (cudaMemcpyToSymbol(g_fa_status, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_CUDA;
     if (v & fa::kStatusTimeout) return FA_ERR_TIMEOUT;
     if (v & fa::kStatusBadSeqlens) return FA_ERR_SEQLENS;
+    if (v & fa::kStatusBadPages) return FA_ERR_PAGES;
   }
   return FA_OK;
 }

@@ -61,7 +61,8 @@ typedef enum {
   FA_ERR_TIMEOUT = 4,
   FA_ERR_WORKSPACE = 5,
   FA_ERR_SCRATCH_TOO_SMALL = 6,
-  FA_ERR_SEQLENS = 7
+  FA_ERR_SEQLENS = 7,
+  FA_ERR_PAGES = 8
 } fa_status;
 
 typedef enum { FA_FP16 = 0, FA_BF16 = 1 } fa_dtype;
@@ -383,6 +384,123 @@ fa_status fa_forward_decode_gqa(const void* q, const void* k, const void* v, voi
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The 8-bit paged K / V cache: fa_paged_append fills it, fa_forward_paged
+ * attends over it and counts where the attention goes, fa_paged_evict drops
+ * the slots that got the least of it.
+ *
+ * k_pages, v_pages: [num_pages, Hkv, page_size, d] 8-bit codes (cache_dtype
+ * FA_E4M3 or FA_E5M2); k_scale, v_scale: [num_pages, Hkv] float32, finite and
+ * >= 0: code c stands for c * scale.  page_table: [B, pages_per_seq] int32:
+ * slot t of sequence b is row t % page_size of page
+ * page_table[b][t / page_size].  All are device pointers, 16-byte aligned;
+ * the struct itself lives on the host and is read during the call only.
+ * page_size in {16, 32, 64, 128}, d in {64, 128, 256}, num_pages * Hkv and
+ * pages_per_seq * page_size < 2^31, B * Hkv <= 65535.
+ *
+ * The filled slots of sequence b are 0 .. lens[b] - 1 (`lens`: [B] device
+ * int32, read on the device).  Calls that change the number of slots write
+ * it to `new_lens`, which must not overlap `lens` (two buffers that take
+ * turns, or a copy).  Table entries past the last filled page are not read.
+ * A sequence whose length is negative or exceeds its bound is treated as
+ * empty (attention) or left as it is (append, evict), and FA_ERR_SEQLENS is
+ * latched for fa_device_status; a table entry outside [0, num_pages) latches
+ * FA_ERR_PAGES and its slots are not seen (attention) or not written
+ * (append), or the sequence is left as it is (evict).  Pages that a call
+ * writes (append: those of the new slots; evict: the first
+ * ceil(keep / page_size) of a sequence) must belong to one sequence only and
+ * stand once in its table; pages that are only read may be shared.
+ *
+ * weight_acc and positions: [B, Hkv, pages_per_seq * page_size], float32 and
+ * int32: for every slot the attention weight it has received, and the
+ * position of the token that it holds.  Slots at and behind the length are
+ * never read; calls write only the slots named at each of them.
+ */
+typedef enum { FA_E4M3 = 0, FA_E5M2 = 1 } fa_cache_dtype;
+
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  float* k_scale;
+  float* v_scale;
+  const int* page_table;
+  int num_pages;
+  int pages_per_seq;
+  int B;
+  int Hkv;
+  int page_size;
+  int d;
+  int cache_dtype;
+} fa_paged_cache;
+
+/*
+ * Append up to N tokens a sequence: k, v: [B, Hkv, N, d] of the 16-bit type
+ * `dtype`; counts: [B] device int32 in [0, N], or NULL (N tokens each).  Token
+ * i of sequence b goes to slot lens[b] + i; new_lens[b] = lens[b] + counts[b]
+ * (at most pages_per_seq * page_size, else FA_ERR_SEQLENS is latched and
+ * new_lens[b] = lens[b]).
+ * Scales, per page and head: s = the smallest power of two >= 2^-100 with
+ * max |x| <= M * s over the page's new elements (M the type's largest
+ * finite code, 448 or 57344); in a page that holds older slots the larger of that and
+ * the page's scale, and if the scale grows the older codes are rounded again
+ * (c * (s_old / s_new)).  Codes are x / s rounded to nearest even.  NaN and
+ * infinities do not count for max |x| and are stored as a cast to the type
+ * stores them (e4m3: NaN).
+ * weight_acc (or NULL): set to 0 for the new slots.  positions (or NULL): set
+ * to first_position[b] + i (first_position: [B] device int32, or NULL: the
+ * slot's number).
+ */
+fa_status fa_paged_append(const fa_paged_cache* cache, const void* k, const void* v, const int* lens,
+                          const int* counts, int* new_lens, float* weight_acc, int* positions,
+                          const int* first_position, int N, int dtype, void* stream);
+
+/*
+ * Attention of Nq queries a sequence over the cache, grouped query heads as in
+ * fa_forward_decode_gqa: q, o: [B, Hq, Nq, d] (dtype), lse: [B, Hq, Nq]
+ * float32.  S = scale * q . (k_scale * k_code) over the slots j < lens[b];
+ * causal: the queries are the last Nq slots, so query i sees the slots
+ * j <= lens[b] - Nq + i.  A query that sees no slot gets O = 0, LSE = -inf.
+ * A K or V element that is not finite reaches the queries that see its slot
+ * as in the formulas; one of V also reaches the other queries of the call
+ * that share its head.
+ * weight_acc (or NULL): the weight exp(S - LSE) of every seen slot, summed over
+ * the Nq queries of the query heads that share the K / V head, is added.
+ * max_len (host int, 0 for pages_per_seq * page_size): bounds the lengths and
+ * sizes the grid.  num_splits: chunks of max_len, 0 picks; at most 1024.
+ * workspace: fa_paged_workspace_size(cache, Hq, Nq, max_len, num_splits,
+ * weight_acc != NULL) bytes, 256-byte aligned, contents irrelevant on entry;
+ * calls that overlap on the GPU need one each.  The size is 0 for invalid
+ * arguments only.
+ * Arithmetic: scores and sums in float32; a query's elements and the softmax
+ * weights enter the 8-bit tensor-core products as sums of e4m3 terms
+ * that hold the 8 (FA_BF16) or 11 (FA_FP16) bits of the 16-bit type.  Results
+ * do not depend on the order in which the GPU runs the chunks.
+ */
+size_t fa_paged_workspace_size(const fa_paged_cache* cache, int Hq, int Nq, int max_len, int num_splits, int weights);
+fa_status fa_forward_paged(const fa_paged_cache* cache, const void* q, const int* lens, void* o, float* lse,
+                           float* weight_acc, int Hq, int Nq, int dtype, int causal, float scale, int max_len,
+                           int num_splits, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Evict, per sequence and head, down to `keep` slots (sequences of at most
+ * `keep` slots stay as they are): new_lens[b] = min(lens[b], keep).  Protected
+ * are the slots whose position lies within the last `recent`, counted from the
+ * head's largest position (0 <= recent <= keep); then those of largest
+ * weight_acc stay (a NaN counts as largest, equal weights: the lowest slots).
+ * The heads of a sequence choose apart.  Kept slots behind the new length
+ * move into the holes before it, the i-th into the i-th hole, with their
+ * codes, weight_acc and positions; slots that stay are not moved, and slots
+ * behind the new length are left as they were.  So the order of the slots is
+ * no longer that of the tokens, which attention does not need: later
+ * tokens are appended behind all of them, and `positions` remembers.  A page
+ * that receives slots takes the largest scale among the slots that it then
+ * holds; codes whose scale was smaller are rounded again (c * (s_old / s_new)).
+ * workspace: fa_paged_evict_workspace_size(cache, keep) bytes, 256-byte aligned.
+ */
+size_t fa_paged_evict_workspace_size(const fa_paged_cache* cache, int keep);
+fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, int* new_lens, float* weight_acc,
+                         int* positions, int keep, int recent, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Size of the fixed device scratch array used by fa_backward_noalloc.
  */
 #define FA_NOALLOC_SCRATCH_BYTES ((size_t)32 << 20)
@@ -412,8 +530,9 @@ fa_status fa_backward_noalloc(const void* q, const void* k, const void* v, const
 /*
  * Waits for all work queued on `stream`, then returns and clears the device
  * status word of the library on the current device: FA_OK, FA_ERR_TIMEOUT if
- * a kernel gave up waiting since the last call, or FA_ERR_CUDA if the
- * stream reports an error.  The only entry point that blocks the host.
+ * a kernel gave up waiting since the last call, FA_ERR_SEQLENS or
+ * FA_ERR_PAGES if one met lengths or page numbers out of range (the first
+ * of these that applies), or FA_ERR_CUDA if the stream reports an error.  The only entry point that blocks the host.
  */
 fa_status fa_device_status(void* stream);
 

@@ -17,6 +17,7 @@ Modules
                published definition) and the keep mask it defines.
 ``varlen``     packed variable-length sequences: each sequence an independent
                problem, bottom-right causal alignment when Nq != Nk.
+``paged``      the 8-bit paged K/V cache: codes, append, attention, eviction.
 
 Every function cites the page passage it follows.  Pages are named by title:
 
@@ -34,4 +35,4 @@ scalar evaluation of the counter mapping, binomial bounds on the keep
 fraction, and torch float64 autograd with the keep mask as a constant.
 No function is "parity unpinned".
 """
-from . import attention, dropout, online, varlen  # noqa: F401
+from . import attention, dropout, online, paged, varlen  # noqa: F401
