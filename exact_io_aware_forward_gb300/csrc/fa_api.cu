@@ -358,6 +358,12 @@ fa_status run_backward(const Shape& s, const void* q, const void* k, const void*
 namespace fa {
 unsigned int* device_status_word() { return status_word(); }
 
+int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
 bool encode_tiled_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const cuuint64_t (&dims)[3],
                       const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();

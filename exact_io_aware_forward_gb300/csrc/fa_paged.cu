@@ -1,12 +1,17 @@
 // Attention over the 8-bit paged K/V cache: few queries a sequence against
 // its slots, split over the slots, grouped query heads.
 //
-// A CTA takes up to R query rows of one K / V head (its query heads' rows are
-// consecutive: rows = group * Nq, row x is query x % Nq) and one chunk of the
-// sequence's slots, and runs the online-softmax recurrence ("FlashAttention
-// 为什么不需要存下注意力矩阵", jefxiong.cn, section 3.2) over tiles of 128 slots.
-// The chunk's normalised O_s (float32) and LSE_s (log2 units) go to the
-// workspace; paged_combine_kernel merges the chunks exactly.
+// A CTA takes up to R = 8 G query rows of a K / V head (its query heads' rows
+// are consecutive: rows = group * Nq, row x is query x % Nq) and runs the
+// online-softmax recurrence ("FlashAttention 为什么不需要存下注意力矩阵",
+// jefxiong.cn, section 3.2) over tiles of 128 slots.  The tiles of all
+// sequences and heads, in order, are shared out evenly among the CTAs that the
+// GPU holds at once, by the lengths on the device: a CTA's run of tiles is cut
+// into segments at the heads' ends, and the pipeline runs on across them.  A
+// segment that is not a whole head leaves its normalised O_s (float32) and
+// LSE_s (log2 units) in the workspace; paged_finish_kernel merges them
+// exactly.  (With num_splits the chunks are cut from max_len instead, one a
+// CTA, and a sequence's result does not depend on the others' lengths.)
 //
 // Both products run on the tensor core with the cache's bytes as they lie in
 // memory (tcgen05 kind::f8f6f4), the cache as operand A and the few rows as
@@ -39,8 +44,10 @@
 // sequence may see are overwritten with zeros in shared memory before the
 // product, since a weight of 0 times a NaN would be a NaN.
 //
-// Roles (192 threads): warps 0-3 softmax and epilogue, warp 4 TMA (one copy a
-// page, lane i the i-th page of a tile), warp 5 TMEM and MMA issue.
+// Roles: G groups of four softmax warps, eight rows each; a TMA warp (one copy
+// a page, lane i the i-th page of a tile); a warp for TMEM and MMA issue; a
+// warp that walks the segments ahead of the others and lists their pages, and
+// one that turns their query rows into terms.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -115,6 +122,23 @@ __device__ __forceinline__ uint32_t sw_offset(uint32_t row, uint32_t col) {
   return row * 64u + ((((col >> 4) ^ (row >> 1)) & 3u) << 4) + (col & 15u);
 }
 
+// tma_load_3d for data that is read once: the lines leave L2 first.  K and V
+// would otherwise push out what every CTA needs again and again, page
+// tables, queries and the kernel's own instructions.
+__device__ __forceinline__ uint64_t stream_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_stream_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z,
+                                              uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
@@ -163,86 +187,100 @@ __device__ __forceinline__ void split_terms(float a, float b, uint32_t (&out)[T]
   }
 }
 
-template <int D, int T, int R>
+template <int D, int T, int G>
 struct PagedCfg {
+  static constexpr int R = 8 * G;                     // query rows of a CTA, eight a softmax group
   static constexpr int W = D == 64 ? 64 : 128;        // bytes of a shared-memory row
   static constexpr int HALVES = D == 256 ? 2 : 1;     // 128-feature parts of a K or V tile
   static constexpr int ITEM = 128 * W;                // one ring slot: 128 slots x W bytes
   static constexpr int NB = (T * R + 15) / 16 * 16;   // columns of operand B (multiple of 16 at M = 128)
-  static constexpr int SCOL = NB <= 16 ? 16 : NB <= 32 ? 32 : NB <= 64 ? 64 : 128;
   static constexpr uint32_t COL_S = 0;                // two score buffers
-  static constexpr uint32_t COL_O = 2 * SCOL;         // HALVES accumulators
-  static constexpr uint32_t TMEM_COLS = 4 * SCOL;
-  // Two CTAs on an SM (about 96 KB of K and V in flight each), one where
-  // the TMEM columns are taken up (NB = 96).
-  static constexpr bool ALONE = NB == 96;
+  static constexpr uint32_t COL_O = 2 * NB;           // HALVES accumulators
+  static constexpr int COLS = (2 + HALVES) * NB;
+  static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  // One group: two CTAs on an SM, each with 90 KB or so of K and V in flight.
+  // More groups, or tiles of 64 KB: one CTA with all of the ring.
+  static constexpr int OCC = G == 1 && D <= 128 ? 2 : 1;
+  // Segments prepared ahead: more of them where heads may be short and their queries small.
+  static constexpr int SEGS = 2;
   static constexpr int Q_BYTES = HALVES * NB * W;
   static constexpr int P_BYTES = NB * 128;
-  static constexpr int BUDGET = (ALONE ? 200 : 105) * 1024;
-  static constexpr int NS_MAX = (BUDGET - Q_BYTES - 2 * P_BYTES) / ITEM;
-  static constexpr int NS = NS_MAX < 12 ? NS_MAX : 12;
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_P = Q_BYTES;
+  static constexpr int BUDGET = (OCC == 2 ? 104 : 192) * 1024;
+  static constexpr int NS_MAX = (BUDGET - SEGS * Q_BYTES - 2 * P_BYTES) / ITEM;
+  // 128 KB of K and V under way on an SM are enough to keep HBM busy; more
+  // (192 KB) only made everything else wait longer for memory: 4 x 32 heads of
+  // 32768 slots took 180 us instead of 171, and shorter calls no less.
+  static constexpr int NS_CAP = 128 * 1024 / OCC / ITEM;
+  static constexpr int NS = NS_MAX < NS_CAP ? NS_MAX : NS_CAP;
+  // Half of the slots for K and half for V.  The softmax waits for V of its
+  // tile ahead of the MMA warp, when the products of the tile two before are
+  // done: two tiles of V in the ring keep that wait within one turn of it.
+  static constexpr int NSV = NS / 2 > 2 * HALVES ? NS / 2 : 2 * HALVES;
+  static constexpr int NSK = NS - NSV;
+  static constexpr int OFF_Q = 0;                     // SEGS segments' queries
+  static constexpr int OFF_P = SEGS * Q_BYTES;        // two tiles' weights
   static constexpr int OFF_RING = OFF_P + 2 * P_BYTES;
   static constexpr int OFF_BAR = OFF_RING + NS * ITEM;
-  // ring_full[NS], ring_empty[NS], s_full[2], p_full[2], pv_done[2], exchange[2], o_full, drain
-  static constexpr int NBAR = 2 * NS + 8 + 2;
+  // ring_full[NS], ring_empty[NS] (K's, then V's), s_full[2], p_full[2], pv_done[2], seg_pages[SEGS], seg_ready[SEGS],
+  // seg_free[SEGS], o_free, drain, exchange[G][2]
+  static constexpr int NBAR = 2 * NS + 8 + 3 * SEGS + 2 * G;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;             // TMEM address, abort flag
-  static constexpr int OFF_ROW = (OFF_MISC + 8 + 15) / 16 * 16;   // inverse scale, end of the visible slots
-  static constexpr int OFF_MAX = OFF_ROW + 8 * R;                 // [2][4][R] warp maxima
-  static constexpr int OFF_SUM = OFF_MAX + 32 * R;                // [4][R] warp sums of l
-  static constexpr int OFF_PAGES = OFF_SUM + 16 * R;              // per page: id, K scale, V scale, log2 V scale
-  static constexpr int THREADS = 192;
-  static constexpr int smem(int pages) { return OFF_PAGES + 16 * pages + 1024; }
-  static_assert(NS >= 4 && Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0, "shared memory layout");
+  static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) / 16 * 16;  // segment descriptors of 8 ints
+  static constexpr int OFF_ROW = OFF_DESC + 32 * SEGS;            // per segment: inverse scales, ends of the visible slots
+  static constexpr int OFF_MAX = OFF_ROW + 8 * SEGS * R;                // [G][2][4][8] warp maxima
+  static constexpr int OFF_SUM = OFF_MAX + 32 * R;                // [G][4][8] warp sums of l
+  static constexpr int OFF_PAGES = OFF_SUM + 16 * R;              // per segment and page: id, K scale, V scale
+  static constexpr int WARPS = 4 * G + 4;  // a multiple of four: the SM's four parts get equally many
+  static constexpr int smem(int pages) { return OFF_PAGES + 12 * SEGS * pages + 1024; }
+  static_assert(NSK >= 2 && Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0 && COLS <= 512, "layout");
 };
 
-// Ring position of item `tile` of K or V in the order K0, K1, V0, K2, V1, ...
-__device__ __forceinline__ int v_position(int j, int n) {
-  const int first = n < 2 ? n : 2, pairs = n - first;
-  return j < pairs ? first + 2 * j : first + pairs + j;
-}
-__device__ __forceinline__ void ring_item(int p, int n, bool& is_v, int& tile) {
-  const int first = n < 2 ? n : 2, pairs = n - first;
-  if (p < first) {
-    is_v = false;
-    tile = p;
-  } else if (p - first < 2 * pairs) {
-    is_v = ((p - first) & 1) == 0;
-    tile = is_v ? (p - first) / 2 : (p - first) / 2 + 2;
-  } else {
-    is_v = true;
-    tile = p - first - pairs;
+// How the work is shared out among the CTAs of a row tile.  A head of t > 0
+// tiles (of 128 slots) takes up kHeadCost + t places on a line of all heads;
+// the line is cut into equal pieces, and a CTA gets the tiles whose places lie
+// in its piece.  (The start and end of a head's segment take about as long as
+// kHeadCost tiles.)
+constexpr int kHeadCost = 2;
+struct Share {
+  long long total;  // places
+  int ctas;         // CTAs that get some
+  // 64-bit divisions are slow: 32 bits wherever they are enough
+  __device__ __forceinline__ long long begin(int i) const {
+    const unsigned long long x = (unsigned long long)i * (unsigned long long)total;
+    return x >> 32 ? (long long)(x / (unsigned)ctas) : (long long)((unsigned)x / (unsigned)ctas);
   }
+  // the CTA that place x belongs to: the largest i with begin(i) <= x
+  __device__ __forceinline__ int owner(long long x) const {
+    const unsigned long long y = ((unsigned long long)x + 1) * (unsigned)ctas - 1;
+    int i = (int)(y >> 32 || total >> 32 ? y / (unsigned long long)total : (unsigned)y / (unsigned)total);
+    while (begin(i) > x) --i;
+    while (begin(i + 1) <= x) ++i;
+    return i;
+  }
+};
+__device__ __forceinline__ Share make_share(long long total, const PagedAttnArgs& a) {
+  const long long want = (total + a.min_tiles - 1) / a.min_tiles;
+  Share s;
+  s.total = total;
+  s.ctas = (int)(want < 1 ? 1 : want < a.ctas ? want : a.ctas);
+  return s;
 }
+__device__ __forceinline__ int good_len(int len, int max_len) { return len < 0 || len > max_len ? 0 : len; }
+__host__ __device__ __forceinline__ int places_of(int tiles) { return tiles > 0 ? tiles + kHeadCost : 0; }
 
-template <int D, int T, int R>
-__global__ void __launch_bounds__(192, (PagedCfg<D, T, R>::ALONE ? 1 : 2))
+struct Segment {
+  int bh, first, n, len, part, pages;  // head, first tile, tiles, the sequence's length, part number or -1, pages
+};
+
+template <int D, int T, int G>
+__global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T, G>::OCC))
     paged_attention_kernel(const __grid_constant__ PagedAttnArgs a) {
-  using C = PagedCfg<D, T, R>;
-  const int BH = a.c.B * a.c.Hkv;
-  const int bh = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int b = bh / a.c.Hkv, h = bh % a.c.Hkv;
+  using C = PagedCfg<D, T, G>;
+  constexpr int R = C::R;
   const int row0 = blockIdx.y * R;
   const int nr = min(R, a.rows - row0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch();
-  int len = a.lens[b];
-  if (len < 0 || len > a.max_len) {  // reported; the sequence counts as empty
-    if (threadIdx.x == 0 && split == 0 && h == 0) atomicOr(a.status, kStatusBadSeqlens);
-    len = 0;
-  }
-  const int kb = split * a.chunk;
-  const int ke = min(len, kb + a.chunk);
-  const int n = ke > kb ? (ke - kb + 127) / 128 : 0;
-  const long long out_row = (long long)bh * a.rows + row0;
-  if (n == 0) {
-    if (a.splits == 1) {  // nothing to see: O = 0, LSE = -inf
-      uint16_t* o = static_cast<uint16_t*>(a.o) + out_row * D;
-      for (int e = threadIdx.x; e < nr * D; e += blockDim.x) o[e] = 0;
-      for (int e = threadIdx.x; e < nr; e += blockDim.x) a.lse[out_row + e] = neg_inf();
-    }
-    return;  // the merge knows from the length which chunks there are
-  }
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -254,22 +292,19 @@ __global__ void __launch_bounds__(192, (PagedCfg<D, T, R>::ALONE ? 1 : 2))
   uint64_t* s_full = ring_empty + C::NS;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
-  uint64_t* exchange = pv_done + 2;
-  uint64_t* o_full = exchange + 2;
-  uint64_t* drain = o_full + 1;
+  uint64_t* seg_pages = pv_done + 2;   // a segment's descriptor and page list are there
+  uint64_t* seg_ready = seg_pages + C::SEGS;  // its scales and queries too
+  uint64_t* seg_free = seg_ready + C::SEGS;   // all of them may be overwritten
+  uint64_t* o_free = seg_free + C::SEGS;      // the accumulators have been read
+  uint64_t* drain = o_free + 1;
+  uint64_t* exchange = drain + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  float* s_qinv = reinterpret_cast<float*>(smem + C::OFF_ROW);
-  int* s_end = reinterpret_cast<int*>(smem + C::OFF_ROW) + R;
-  float* s_max = reinterpret_cast<float*>(smem + C::OFF_MAX);
-  float* s_sum = reinterpret_cast<float*>(smem + C::OFF_SUM);
-  const int ps = a.c.ps, shift = a.c.ps_shift;
-  const int ne = (ke - kb + ps - 1) >> shift;  // pages of this chunk
+  const int shift = a.c.ps_shift, ps = a.c.ps;
+  const int ne = a.seg_pages;  // page entries a segment buffer holds
   int* s_page = reinterpret_cast<int*>(smem + C::OFF_PAGES);
-  float* s_ks = reinterpret_cast<float*>(s_page + ne);
-  float* s_vs = s_ks + ne;
-  float* s_lv = s_vs + ne;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* s_ks = reinterpret_cast<float*>(s_page + C::SEGS * ne);
+  float* s_vs = s_ks + C::SEGS * ne;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
@@ -278,162 +313,377 @@ __global__ void __launch_bounds__(192, (PagedCfg<D, T, R>::ALONE ? 1 : 2))
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 4 * G);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&exchange[i], 4);
     }
-    mbar_init(o_full, 1);
+    for (int i = 0; i < C::SEGS; ++i) {
+      mbar_init(&seg_pages[i], 1);
+      mbar_init(&seg_ready[i], 1);
+      mbar_init(&seg_free[i], 4 * G + 1);
+    }
+    mbar_init(o_free, 4 * G);
     mbar_init(drain, 1);
+    for (int i = 0; i < 2 * G; ++i) mbar_init(&exchange[i], 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == 4 * G && lane == 0) {
     tma_prefetch_desc(&a.tm_k);
     tma_prefetch_desc(&a.tm_v);
   }
-  if (warp == 5) {
+  if (warp == 4 * G + 1) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
-  {
-    const int* table = a.c.table + (long long)b * a.c.width + (kb >> shift);
-    for (int i = threadIdx.x; i < ne; i += blockDim.x) {
-      int id = table[i];
-      float ks = 0.f, vs = 0.f;
-      if (id < 0 || id >= a.c.pages) {
-        atomicOr(a.status, kStatusBadPages);
-        id = -1;
-      } else {
-        ks = a.c.k_scale[(long long)id * a.c.Hkv + h];
-        vs = a.c.v_scale[(long long)id * a.c.Hkv + h];
+  // The walker's state, found while the others set up.
+  auto tiles_of = [&](int b) { return (good_len(a.lens[b], a.max_len) + 127) >> 7; };
+  // The next segment: head h of sequence b (tb tiles), its tiles from t on; in the balanced case the head's place
+  // on the line is `at` and this CTA's piece ends at `stop`.
+  int b = 0, h = 0, t = 0, tb = 0, n = 0;
+  long long at = 0, stop = 0;
+  Share share = {1, 1};
+  auto place = [&](long long from) {  // the head's tiles in [from, stop)
+    const long long first = from - at - kHeadCost, last = stop - at - kHeadCost;
+    t = (int)(first > 0 ? first : 0);
+    n = (int)(last < tb ? last : tb) - t;
+  };
+  if (warp == 4 * G + 2) {
+    if (a.balanced) {
+      int mine = 0;  // tiles of sequence `lane` of the last 32 looked at
+      long long total = 0;
+      for (int b0 = 0; b0 < a.c.B; b0 += 32) {
+        const int len = b0 + lane < a.c.B ? a.lens[b0 + lane] : 0;
+        if (good_len(len, a.max_len) != len && blockIdx.x == 0) atomicOr(a.status, kStatusBadSeqlens);
+        mine = (good_len(len, a.max_len) + 127) >> 7;
+        total += __reduce_add_sync(0xffffffffu, (unsigned)places_of(mine));
       }
-      s_page[i] = id;
-      s_ks[i] = ks * a.scale_log2;
-      s_vs[i] = vs;
-      s_lv[i] = fmaxf(__log2f(fabsf(vs)), kMinLogScale);
-    }
-  }
-  // Query rows to e4m3 terms: a warp a row, D / 32 elements a lane.
-  for (int r = warp; r < R; r += C::THREADS / 32) {
-    constexpr int E = D / 32;
-    float x[E];
-    float top = 0.f;
-    bool finite = true;
+      total *= a.c.Hkv;
+      share = make_share(total, a);
+      if (total > 0 && (int)blockIdx.x < share.ctas) {
+        const long long lo = share.begin(blockIdx.x);
+        stop = share.begin(blockIdx.x + 1);
+        for (int b0 = 0; lo < stop; b0 += 32) {
+          if (a.c.B > 32) mine = b0 + lane < a.c.B ? tiles_of(b0 + lane) : 0;
+          int upto = places_of(mine);  // inclusive over the lanes
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = 0.f;
-    if (r < nr) {
-      const long long at = (out_row + r) * D + lane * E;
-#pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const uint32_t two = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at + i);
-        if (a.bf16) {
-          x[i] = __uint_as_float(two << 16);
-          x[i + 1] = __uint_as_float(two & 0xffff0000u);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-          x[i] = f.x;
-          x[i + 1] = f.y;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, at + (long long)upto * a.c.Hkv > lo);
+          if (past) {
+            const int l = __ffs(past) - 1;
+            tb = __shfl_sync(0xffffffffu, mine, l);
+            at += (long long)(__shfl_sync(0xffffffffu, upto, l) - places_of(tb)) * a.c.Hkv;
+            b = b0 + l;
+            break;
+          }
+          at += (long long)__shfl_sync(0xffffffffu, upto, 31) * a.c.Hkv;
+        }
+        if (lo < stop) {
+          const long long in = lo - at;  // less than Hkv heads of 2^24 tiles each, mostly much less
+          h = in >> 32 ? (int)(in / places_of(tb)) : (int)((unsigned)in / (unsigned)places_of(tb));
+          at += (long long)h * places_of(tb);
+          place(lo);
         }
       }
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        finite = finite && isfinite(x[i]);
-        top = fmaxf(top, fabsf(x[i]));
+    } else {
+      const int bh = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+      b = bh / a.c.Hkv;
+      h = bh % a.c.Hkv;
+      const int len = a.lens[b];
+      if (good_len(len, a.max_len) != len && h == 0 && split == 0) atomicOr(a.status, kStatusBadSeqlens);
+      tb = tiles_of(b);
+      t = split * a.per;
+      n = min(a.per, tb - t);
+      if (tb == 0 && a.splits == 1) {  // nothing to see: O = 0, LSE = -inf
+        const long long out_row = (long long)bh * a.rows + row0;
+        uint16_t* o = static_cast<uint16_t*>(a.o) + out_row * D;
+        for (int e = lane; e < nr * D; e += 32) o[e] = 0;
+        for (int e = lane; e < nr; e += 32) a.lse[out_row + e] = neg_inf();
       }
     }
-    finite = __all_sync(0xffffffffu, finite);
-    top = warp_max(top);
-    // 2^e with top * 2^e in [128, 256) (subnormal rows: at most 2^120)
-    const int e = min(134 - static_cast<int>(__float_as_uint(top) >> 23), 120);
-    const float up = __int_as_float((e + 127) << 23);
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      uint32_t code[T];
-      split_terms<T>(finite ? x[i] * up : 0.f, finite ? x[i + 1] * up : 0.f, code);
-      const int col = lane * E + i;
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-        *reinterpret_cast<uint16_t*>(sQ + (col / C::W) * (C::NB * C::W) + sw_offset<C::W>(t * R + r, col % C::W)) =
-            static_cast<uint16_t>(code[t]);
-    }
-    if (lane == 0) {
-      // a row that holds a NaN or an infinity has no softmax: its scores are NaN
-      s_qinv[r] = finite ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fc00000);
-      s_end[r] = a.causal ? len - a.Nq + (row0 + r) % a.Nq + 1 : len;
-    }
   }
-  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  auto read_segment = [&](int k) {
+    const int4 x = *reinterpret_cast<const int4*>(smem + C::OFF_DESC + 32 * (k % C::SEGS));
+    const int2 y = *reinterpret_cast<const int2*>(smem + C::OFF_DESC + 32 * (k % C::SEGS) + 16);
+    Segment g;
+    g.bh = x.x, g.first = x.y, g.n = x.z, g.len = x.w, g.part = y.x, g.pages = y.y;
+    return g;
+  };
 
-  if (warp == 4) {
-    // ------------------------------------------------------------ producer
-    const int per = 128 >> shift;  // pages a tile
-    const int items = 2 * n * C::HALVES;
-    int issued = 0;
-    for (int p = 0; p < items; ++p) {
-      const int slot = p % C::NS;
-      if (!warp_wait(&ring_empty[slot], ((p / C::NS) & 1) ^ 1, abort_flag, a.status)) break;
-      bool is_v;
-      int t;
-      ring_item(p / C::HALVES, n, is_v, t);
-      const int half = p % C::HALVES;
-      const int e = t * per + lane;
-      const int id = lane < per && e < ne ? s_page[e] : -1;
-      const unsigned there = __ballot_sync(0xffffffffu, id >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(&ring_full[slot], __popc(there) * ps * C::W);
-      __syncwarp();
-      if (id >= 0)
-        tma_load_3d(sRing + slot * C::ITEM + lane * ps * C::W, is_v ? &a.tm_v : &a.tm_k, &ring_full[slot], half * 128,
-                    0, id * a.c.Hkv + h);
-      issued = p + 1;
+  if (warp == 4 * G + 2) {
+    // ------------------------------------------------------------ segments
+    // Walks this CTA's tiles segment by segment (a run of tiles of one head),
+    // ahead of the others: where each one is, and its pages.
+    // To the next head that has tiles in this CTA's piece; n = 0 when there is none.
+    auto advance = [&]() {
+      do {
+        n = 0;
+        at += places_of(tb);
+        if (!a.balanced || at >= stop) return;
+        if (++h == a.c.Hkv) {
+          h = 0;
+          do tb = tiles_of(++b);
+          while (tb == 0);
+        }
+        place(at);
+      } while (n <= 0);
+    };
+    if (n <= 0) {
+      n = 0;
+      if (a.balanced && at < stop) advance();
     }
-    if (*abort_flag && lane == 0)
-      for (int p = issued - C::NS < 0 ? 0 : issued - C::NS; p < issued; ++p)
-        drain_wait(&ring_full[p % C::NS], (uint32_t)((p / C::NS) & 1));
+    for (int k = 0;; ++k) {
+      const int buf = k % C::SEGS;
+      if (k >= C::SEGS && !warp_wait(&seg_free[buf], (k / C::SEGS - 1) & 1, abort_flag, a.status)) break;
+      const int bh = b * a.c.Hkv + h;
+      const int len = n > 0 ? good_len(a.lens[b], a.max_len) : 0;
+      const int end = min(len, (t + n) * 128);  // one past the segment's last slot
+      const int pages = n > 0 ? (end - t * 128 + ps - 1) >> shift : 0;
+      if (lane == 0) {
+        int* d = reinterpret_cast<int*>(smem + C::OFF_DESC + 32 * buf);
+        d[0] = bh, d[1] = t, d[2] = n, d[3] = len;
+        // a whole head goes to O; a CTA has at most two parts of heads: one that ends in it, one that begins
+        d[4] = n == tb ? -1 : (int)(2 * (blockIdx.y * gridDim.x + blockIdx.x)) + (a.balanced && t == 0 ? 1 : 0);
+        d[5] = pages;
+      }
+      const int* table = a.c.table + (long long)b * a.c.width + (t * 128 >> shift);
+      for (int i = lane; i < pages; i += 32) {
+        int id = table[i];
+        if (id < 0 || id >= a.c.pages) {
+          atomicOr(a.status, kStatusBadPages);
+          id = -1;
+        }
+        s_page[buf * ne + i] = id;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_pages[buf]);
+      if (n == 0) break;
+      if (a.balanced && t == 0 && lane == 0 && blockIdx.y == 0) {
+        // for the joining kernel: how many CTAs share the head, and the first of them
+        const int count = n == tb ? 1 : share.owner(at + kHeadCost + tb - 1) - (int)blockIdx.x + 1;
+        a.shared[bh] = make_int2(count, blockIdx.x);
+      }
+      advance();
+    }
+  } else if (warp == 4 * G + 3) {
+    // ------------------------------------------------------------ scales and queries
+    // Turns the segment's query rows into e4m3 terms and fetches its scales:
+    // four rows at a time, eight lanes a row, the next four on their way.  The
+    // row loop is kept rolled: instructions that run once cost more to fetch
+    // than to run.
+    constexpr int E = D / 8;   // neighbouring elements of a row a lane
+    constexpr int L = E / 8;   // 16-byte loads of them
+    const int sub = lane >> 3, col = (lane & 7) * E;
+    for (int k = 0;; ++k) {
+      const int buf = k % C::SEGS;
+      if (!warp_wait(&seg_pages[buf], (k / C::SEGS) & 1, abort_flag, a.status)) break;
+      const Segment g = read_segment(k);
+      const int head = g.bh % a.c.Hkv;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((long long)g.bh * a.rows + row0) * D + col;
+      uint8_t* q8 = sQ + buf * C::Q_BYTES + (col / C::W) * (C::NB * C::W);
+      float* qinv = reinterpret_cast<float*>(smem + C::OFF_ROW) + buf * 2 * R;
+      int* row_end = reinterpret_cast<int*>(qinv + R);
+      uint4 raw[L], then[L];
+      auto load = [&](int r, uint4 (&to)[L]) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          to[i] = r < nr && g.n > 0 ? reinterpret_cast<const uint4*>(q + (long long)r * D)[i] : make_uint4(0, 0, 0, 0);
+      };
+      load(sub, raw);
+      for (int i = lane; g.n > 0 && i < g.pages; i += 32) {
+        const int id = s_page[buf * ne + i];
+        s_ks[buf * ne + i] = id >= 0 ? a.c.k_scale[(long long)id * a.c.Hkv + head] * a.scale_log2 : 0.f;
+        s_vs[buf * ne + i] = id >= 0 ? a.c.v_scale[(long long)id * a.c.Hkv + head] : 0.f;
+      }
+#pragma unroll 1
+      for (int r = sub; g.n > 0 && r < R; r += 4) {
+        load(r + 4, then);
+        float x[E];
+        uint32_t top = 0;  // the largest magnitude's bits: infinities and NaN come out on top
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const uint4& u = raw[i / 8];
+          const uint32_t two = i % 8 == 0 ? u.x : i % 8 == 2 ? u.y : i % 8 == 4 ? u.z : u.w;
+          if (a.bf16) {
+            x[i] = __uint_as_float(two << 16);
+            x[i + 1] = __uint_as_float(two & 0xffff0000u);
+          } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+            x[i] = f.x;
+            x[i + 1] = f.y;
+          }
+          top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(x[i + 1]) & 0x7fffffffu));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool finite = top < 0x7f800000u;
+        // 2^e with max * 2^e in [128, 256) (subnormal rows: at most 2^120)
+        const int e = finite ? min(134 - static_cast<int>(top >> 23), 120) : 0;
+        const float up = __int_as_float((e + 127) << 23);
+        uint32_t words[T][E / 4];
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+          uint32_t lo[T], hi[T];
+          split_terms<T>(finite ? x[i] * up : 0.f, finite ? x[i + 1] * up : 0.f, lo);
+          split_terms<T>(finite ? x[i + 2] * up : 0.f, finite ? x[i + 3] * up : 0.f, hi);
+#pragma unroll
+          for (int u = 0; u < T; ++u) words[u][i / 4] = lo[u] | hi[u] << 16;
+        }
+#pragma unroll
+        for (int u = 0; u < T; ++u) {
+          if constexpr (E == 8) {
+            *reinterpret_cast<uint2*>(q8 + sw_offset<C::W>(u * R + r, col % C::W)) = make_uint2(words[u][0], words[u][1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < E / 16; ++i)
+              *reinterpret_cast<uint4*>(q8 + sw_offset<C::W>(u * R + r, col % C::W + 16 * i)) =
+                  make_uint4(words[u][4 * i], words[u][4 * i + 1], words[u][4 * i + 2], words[u][4 * i + 3]);
+          }
+        }
+        if ((lane & 7) == 0) {
+          // a row that holds a NaN or an infinity has no softmax: its scores are NaN
+          qinv[r] = finite ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fc00000);
+          row_end[r] = a.causal ? g.len - a.Nq + (row0 + r) % a.Nq + 1 : g.len;
+        }
+#pragma unroll
+        for (int i = 0; i < L; ++i) raw[i] = then[i];
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_ready[buf]);
+      if (g.n == 0) break;
+    }
+  } else if (warp == 4 * G) {
+    // ------------------------------------------------------------ producer
+    // Tiles in the order K0, K1, V0, K2, V1, ... over all segments.
+    const int per = 128 >> shift;  // pages a tile
+    bool ok = true;
+    struct Cursor {
+      int k = -1, t = 0, n = 0, h = 0, end = 0;
+    } kc, vc;
+    // to the next tile: false when there is none (or on abort)
+    auto next = [&](Cursor& c) {
+      if (++c.t < c.n) return true;
+      ++c.k;
+      if (!(ok = warp_wait(&seg_pages[c.k % C::SEGS], (c.k / C::SEGS) & 1, abort_flag, a.status))) return false;
+      const Segment g = read_segment(c.k);
+      c.t = 0;
+      c.n = g.n;
+      c.h = g.bh % a.c.Hkv;
+      c.end = g.pages;
+      return g.n > 0;
+    };
+    const uint64_t policy = stream_policy();
+    int pk = 0, pv = 0;  // items of K and V issued
+    auto load = [&](const Cursor& c, const CUtensorMap* map, int& p, int first, int slots) {
+      const int e = c.t * per + lane;
+      const int id = lane < per && e < c.end ? s_page[(c.k % C::SEGS) * ne + e] : -1;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * ps * C::W;
+      for (int hf = 0; hf < C::HALVES; ++hf, ++p) {
+        const int slot = first + p % slots;
+        if (!(ok = warp_wait(&ring_empty[slot], ((p / slots) & 1) ^ 1, abort_flag, a.status))) return;
+        if (lane == 0) mbar_arrive_expect_tx(&ring_full[slot], bytes);
+        __syncwarp();
+        if (id >= 0)
+          tma_stream_3d(sRing + slot * C::ITEM + lane * ps * C::W, map, &ring_full[slot], hf * 128, 0,
+                        id * a.c.Hkv + c.h, policy);
+      }
+    };
+    // a segment's list is waited for only when V of the tile two before is on
+    // its way: the list two segments on needs the place of that tile's
+    bool more = true;
+    auto load_k = [&]() {
+      more = more && next(kc);
+      if (more) load(kc, &a.tm_k, pk, 0, C::NSK);
+    };
+    load_k();
+    if (ok) load_k();
+    while (ok && next(vc)) {
+      load(vc, &a.tm_v, pv, C::NSK, C::NSV);
+      if (!ok) break;
+      if (vc.t == vc.n - 1 && lane == 0) mbar_arrive(&seg_free[vc.k % C::SEGS]);
+      load_k();
+    }
+    if (*abort_flag && lane == 0) {
+      for (int x = pk - C::NSK < 0 ? 0 : pk - C::NSK; x < pk; ++x)
+        drain_wait(&ring_full[x % C::NSK], (uint32_t)((x / C::NSK) & 1));
+      for (int x = pv - C::NSV < 0 ? 0 : pv - C::NSV; x < pv; ++x)
+        drain_wait(&ring_full[C::NSK + x % C::NSV], (uint32_t)((x / C::NSV) & 1));
+    }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 4 * G + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t id_s = idesc_f8(128, C::NB, a.c.e5m2, false);
       const uint32_t id_pv = idesc_f8(128, C::NB, a.c.e5m2, true);
       const uint32_t q = smem_u32(sQ), pw = smem_u32(sP), ring = smem_u32(sRing);
       constexpr int GROUP = 8 * C::W;  // eight rows: the stride of the swizzle pattern
-      int p = 0;
-      auto take = [&](int& slot) {
-        slot = p % C::NS;
-        const bool ok = mbar_wait(&ring_full[slot], (p / C::NS) & 1, abort_flag, a.status, kStatusTimeout);
+      bool ok = true;
+      int pk = 0, pv = 0;
+      auto take = [&](int& slot, int& p, int first, int slots) {
+        slot = first + p % slots;
+        ok = mbar_wait(&ring_full[slot], (p / slots) & 1, abort_flag, a.status, kStatusTimeout);
         ++p;
         tc_fence_after();
         return ok;
       };
-      // S buffer i: slots as rows (K-major A), query terms as columns
-      auto issue_s = [&](int i) {
+      int sk = -1, st = 0, sn = 0, sj = 0;  // next score tile: segment, tile in it, its tiles; tile over all
+      bool more = true;
+      // the tiles of the segments whose scores are under way, in words of the
+      // descriptors that are this thread's own: a descriptor itself may be
+      // overwritten as soon as the softmax is done with the segment
+      auto tiles_in = [&](int k) -> volatile int& {
+        return *reinterpret_cast<volatile int*>(smem + C::OFF_DESC + 32 * (k % C::SEGS) + 24 + 4 * ((k / C::SEGS) & 1));
+      };
+      // S of the next tile: slots as rows (K-major A), query terms as columns
+      auto issue_s = [&]() {
+        if (++st >= sn) {
+          ++sk;
+          if (!(ok = mbar_wait(&seg_ready[sk % C::SEGS], (sk / C::SEGS) & 1, abort_flag, a.status, kStatusTimeout))) return;
+          st = 0;
+          sn = read_segment(sk).n;
+          if (sn == 0) {
+            more = false;
+            return;
+          }
+          tiles_in(sk) = sn;
+        }
+        const int i = sj & 1;
         for (int hf = 0; hf < C::HALVES; ++hf) {
           int slot;
-          if (!take(slot)) return false;
+          if (!take(slot, pk, 0, C::NSK)) return;
           const uint64_t da = sdesc_w<C::W>(ring + slot * C::ITEM, 16, GROUP);
-          const uint64_t db = sdesc_w<C::W>(q + hf * C::NB * C::W, 16, GROUP);
+          const uint64_t db = sdesc_w<C::W>(q + (sk % C::SEGS) * C::Q_BYTES + hf * C::NB * C::W, 16, GROUP);
 #pragma unroll
           for (int kk = 0; kk < C::W / 32; ++kk)
-            mma_f8(tmem + C::COL_S + C::SCOL * i, sdesc_advance(da, 32 * kk), sdesc_advance(db, 32 * kk), id_s,
+            mma_f8(tmem + C::COL_S + C::NB * i, sdesc_advance(da, 32 * kk), sdesc_advance(db, 32 * kk), id_s,
                    hf > 0 || kk > 0);
           mma_commit(&ring_empty[slot]);
         }
         mma_commit(&s_full[i]);
-        return true;
+        ++sj;
       };
-      bool ok = issue_s(0);
-      if (ok && n > 1) ok = issue_s(1);
-      for (int j = 0; ok && j < n; ++j) {
+      issue_s();
+      if (ok && more) issue_s();
+      int vk = 0, vt = 0, vn = 0;  // segment and tile of PV
+      for (int j = 0; ok && j < sj; ++j) {
         const int i = j & 1;
+        if (vt == 0) vn = tiles_in(vk);
         if (!(ok = mbar_wait(&p_full[i], (j >> 1) & 1, abort_flag, a.status, kStatusTimeout))) break;
+        // a segment's first product overwrites what the one before left for its epilogue
+        if (vt == 0 && vk > 0 &&
+            !(ok = mbar_wait(o_free, (vk - 1) & 1, abort_flag, a.status, kStatusTimeout)))
+          break;
         tc_fence_after();
         for (int hf = 0; hf < C::HALVES; ++hf) {
           int slot;
-          if (!(ok = take(slot))) break;
+          if (!take(slot, pv, C::NSK, C::NSV)) break;
           // features as rows (MN-major A: a row of memory is a slot); at
           // d = 64 both 64-feature halves of M = 128 read the same bytes
           // (offset 0 between them), lanes 64-127 repeat lanes 0-63
@@ -441,17 +691,19 @@ __global__ void __launch_bounds__(192, (PagedCfg<D, T, R>::ALONE ? 1 : 2))
           const uint64_t db = sdesc_w<128>(pw + i * C::P_BYTES, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f8(tmem + C::COL_O + C::SCOL * hf, sdesc_advance(da, 32 * C::W * kk), sdesc_advance(db, 32 * kk),
-                   id_pv, j > 0 || kk > 0);
+            mma_f8(tmem + C::COL_O + C::NB * hf, sdesc_advance(da, 32 * C::W * kk), sdesc_advance(db, 32 * kk),
+                   id_pv, vt > 0 || kk > 0);
           mma_commit(&ring_empty[slot]);
         }
         if (!ok) break;
         mma_commit(&pv_done[i]);
-        if (j + 2 < n) ok = issue_s(i);
+        if (++vt == vn) {
+          vt = 0;
+          ++vk;
+        }
+        if (more) issue_s();
       }
-      if (ok) {
-        mma_commit(o_full);
-      } else {
+      if (!ok) {
         mma_commit(drain);
         drain_wait(drain, 0);
       }
@@ -459,310 +711,424 @@ __global__ void __launch_bounds__(192, (PagedCfg<D, T, R>::ALONE ? 1 : 2))
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax, epilogue
-    const int key = warp * 32 + lane;  // slot of the tile
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    float l[R], m[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      l[r] = 0.f;
-      m[r] = neg_inf();
-    }
-    // bytes of P: row t * R + r of 128 slots
-    uint32_t p_at[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) p_at[r] = smem_u32(sP) + sw_offset<128>(r, key);
-    const int first_end = a.causal ? len - a.Nq + 1 : len;  // the fewest slots that a row sees
+    // Group g of four warps: rows 8 g .. 8 g + 7; warp w of it: slots 32 w .. 32 w + 31 of a tile.
+    const int g8 = (warp >> 2) * 8, quarter = warp & 3;
+    const int key = quarter * 32 + lane;  // slot of the tile
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint64_t* my_exchange = exchange + (warp >> 2) * 2;
+    float* my_max = reinterpret_cast<float*>(smem + C::OFF_MAX) + (warp >> 2) * 64;
+    float* my_sum = reinterpret_cast<float*>(smem + C::OFF_SUM) + (warp >> 2) * 32;
+    // byte of this slot in row r of the weights, r = 0 .. 7 of the group
+    const uint32_t p_row = smem_u32(sP) + g8 * 128 + (key & 15);
+    const int chunk16 = key >> 4;
+    int j = 0;  // tile over all segments
+    int x = 0;  // exchanges so far
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int i = j & 1;
-      const uint32_t tS = lane_base + C::COL_S + C::SCOL * i;
-      const int slot = kb + j * 128 + key;
-      const int e = (j * 128 + key) >> shift;
-      const bool live = slot < ke && s_page[e] >= 0;
-      const float ks = live ? s_ks[e] : 0.f, vs = live ? s_vs[e] * kWeightScale : 0.f, lv = live ? s_lv[e] : 0.f;
-      if (!(ok = warp_wait(&s_full[i], (j >> 1) & 1, abort_flag, a.status))) break;
-      tc_fence_after();
-      const bool cut = kb + j * 128 + 128 > first_end;  // some row sees less than the tile
-      float s[R];
+    for (int k = 0;; ++k) {
+      if (!(ok = warp_wait(&seg_ready[k % C::SEGS], (k / C::SEGS) & 1, abort_flag, a.status))) break;
+      const Segment g = read_segment(k);
+      if (g.n == 0) break;
+      const int buf = k % C::SEGS;
+      const int* page = s_page + buf * ne;
+      const float* qinv = reinterpret_cast<const float*>(smem + C::OFF_ROW) + buf * 2 * R + g8;
+      const int* row_end = reinterpret_cast<const int*>(qinv + R);
+      const int first_end = a.causal ? g.len - a.Nq + 1 : g.len;  // the fewest slots that a row sees
+      const long long out_row = (long long)g.bh * a.rows + row0 + g8;
+      const int rows_here = nr - g8;
+      float* scores = a.scores + ((long long)g.bh * a.score_groups + (row0 + g8) / 8) * a.score_stride;
+      float l[8], m[8];
 #pragma unroll
-      for (int c = 0; c < R; c += 8) {
-        float x[T][8];
-#pragma unroll
-        for (int t = 0; t < T; ++t) tmem_ld8(tS + t * R + c, x[t]);
-#pragma unroll
-        for (int t = 0; t < T; ++t) tmem_ld8_wait(x[t]);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          float y = x[T - 1][r];
-#pragma unroll
-          for (int t = T - 2; t >= 0; --t) y = fmaf(y, 0.0625f, x[t][r]);
-          s[c + r] = y * s_qinv[c + r] * ks;
-        }
+      for (int r = 0; r < 8; ++r) {
+        l[r] = 0.f;
+        m[r] = neg_inf();
       }
-      if (cut || !live) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (!live || slot >= s_end[r]) s[r] = neg_inf();
-      }
-      if (a.scores != nullptr && slot < ke) {
-        float* to = a.scores + out_row * a.score_stride + slot;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (r < nr) to[r * a.score_stride] = s[r];
-      }
-      float* mine = s_max + (i * 4 + warp) * R;
-#pragma unroll
-      for (int r = 0; r < R; r += 4) {
-        float4 x;
-        x.x = warp_max(s[r] + lv);
-        x.y = warp_max(s[r + 1] + lv);
-        x.z = warp_max(s[r + 2] + lv);
-        x.w = warp_max(s[r + 3] + lv);
-        if (lane == 0) *reinterpret_cast<float4*>(mine + r) = x;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&exchange[i]);
-      if (!(ok = warp_wait(&exchange[i], (j >> 1) & 1, abort_flag, a.status))) break;
-      // every thread derives the same new references from the four warps' maxima
-      float corr[R];
-      bool moved = false;
-      const float* all = s_max + i * 4 * R;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float x = fmaxf(fmaxf(all[r], all[R + r]), fmaxf(all[2 * R + r], all[3 * R + r]));
-        corr[r] = 1.f;
-        if (x > m[r] + kMaxLead) {
-          corr[r] = ex2_approx(m[r] - x);
-          l[r] *= corr[r];
-          m[r] = x;
-          moved = true;
-        }
-      }
-      if (moved && j > 0) {  // the same on every thread; PV(j - 1) may still add to O
-        if (!(ok = warp_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, a.status))) break;
+      for (int t = 0; t < g.n; ++t, ++j) {
+        const int i = j & 1;
+        const uint32_t tS = lane_base + C::COL_S + C::NB * i + g8;
+        const int slot = (g.first + t) * 128 + key;
+        const int e = buf * ne + ((t * 128 + key) >> shift);
+        const bool live = slot < g.len && page[(t * 128 + key) >> shift] >= 0;
+        const float ks = live ? s_ks[e] : 0.f, vs = live ? s_vs[e] : 0.f;
+        const float lv = fmaxf(__log2f(fabsf(vs)), kMinLogScale), wv = vs * kWeightScale;
+        if (!(ok = warp_wait(&s_full[i], (j >> 1) & 1, abort_flag, a.status))) break;
         tc_fence_after();
+        float s[8];
+        {
+          float y[T][8];
 #pragma unroll
-        for (int hf = 0; hf < C::HALVES; ++hf)
+          for (int u = 0; u < T; ++u) tmem_ld8(tS + u * R, y[u]);
 #pragma unroll
-          for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int c = 0; c < R; c += 8) {
-              float x[8];
-              const uint32_t at = lane_base + C::COL_O + C::SCOL * hf + t * R + c;
-              tmem_ld8(at, x);
-              tmem_ld8_wait(x);
-              uint32_t y[8];
-#pragma unroll
-              for (int r = 0; r < 8; ++r) y[r] = __float_as_uint(x[r] * corr[c + r]);
-              tmem_st8(at, y);
-            }
-        tmem_st_wait();
-      }
-      const uint32_t pbuf = i * C::P_BYTES;
-#pragma unroll
-      for (int r = 0; r < R; r += 2) {
-        const float p0 = ex2_approx(s[r] - (m[r] == neg_inf() ? 0.f : m[r]));
-        const float p1 = ex2_approx(s[r + 1] - (m[r + 1] == neg_inf() ? 0.f : m[r + 1]));
-        l[r] += p0;
-        l[r + 1] += p1;
-        uint32_t code[T];
-        split_terms<T>(p0 * vs, p1 * vs, code);
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-          const uint32_t at = pbuf + (t * R + (r & ~7)) * 128;
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(p_at[r & 7] + at), "r"(code[t] & 0xffu) : "memory");
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(p_at[(r & 7) + 1] + at), "r"(code[t] >> 8) : "memory");
-        }
-      }
-      if (!live) {  // no bytes of this slot may reach the product
-        for (int hf = 0; hf < C::HALVES; ++hf) {
-          const int p = v_position(j, n) * C::HALVES + hf;
-          if (!mbar_wait(&ring_full[p % C::NS], (p / C::NS) & 1, abort_flag, a.status, kStatusTimeout)) ok = false;
-          uint4* row = reinterpret_cast<uint4*>(sRing + (p % C::NS) * C::ITEM + key * C::W);
-          if (ok)
-            for (int x = 0; x < C::W / 16; ++x) row[x] = make_uint4(0, 0, 0, 0);
-        }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      if (lane == 0) mbar_arrive(&p_full[i]);
-    }
-    // l over the 128 slots of a tile: lanes, then warps
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float x = warp_sum(l[r]);
-      if (lane == 0) s_sum[warp * R + r] = x;
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&exchange[n & 1]);
-    if (ok) ok = warp_wait(&exchange[n & 1], (n >> 1) & 1, abort_flag, a.status);
-    if (ok) ok = warp_wait(o_full, 0, abort_flag, a.status);
-    if (ok) {
-      tc_fence_after();
-      const long long part = ((long long)split * BH * a.rows + out_row) * D;
-#pragma unroll
-      for (int c = 0; c < R; c += 8) {
-        if (c >= nr) break;
-        float inv[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float x = s_sum[c + r] + s_sum[R + c + r] + s_sum[2 * R + c + r] + s_sum[3 * R + c + r];
-          inv[r] = x == 0.f ? 0.f : (1.f / kWeightScale) / x;
-          if (threadIdx.x == 0 && c + r < nr) {
-            const float lse2 = x == 0.f ? neg_inf() : (m[c + r] == neg_inf() ? 0.f : m[c + r]) + __log2f(x);
-            if (a.splits == 1)
-              a.lse[out_row + c + r] = lse2 * kLn2;
-            else
-              a.lse_part[(long long)split * BH * a.rows + out_row + c + r] = lse2;
-          }
-        }
-#pragma unroll
-        for (int hf = 0; hf < C::HALVES; ++hf) {
-          float x[T][8];
-#pragma unroll
-          for (int t = 0; t < T; ++t) tmem_ld8(lane_base + C::COL_O + C::SCOL * hf + t * R + c, x[t]);
-#pragma unroll
-          for (int t = 0; t < T; ++t) tmem_ld8_wait(x[t]);
-          const int f = hf * 128 + key;
+          for (int u = 0; u < T; ++u) tmem_ld8_wait(y[u]);
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            float y = x[T - 1][r];
+            float z = y[T - 1][r];
 #pragma unroll
-            for (int t = T - 2; t >= 0; --t) y = fmaf(y, 0.0625f, x[t][r]);
-            y *= inv[r];
-            if (c + r < nr && f < D) {
-              if (a.splits != 1) {
-                a.o_part[part + (long long)(c + r) * D + f] = y;
-              } else if (a.bf16) {
-                static_cast<__nv_bfloat16*>(a.o)[(out_row + c + r) * D + f] = __float2bfloat16_rn(y);
-              } else {
-                static_cast<__half*>(a.o)[(out_row + c + r) * D + f] = __float2half_rn(y);
-              }
+            for (int u = T - 2; u >= 0; --u) z = fmaf(z, 0.0625f, y[u][r]);
+            s[r] = z * qinv[r] * ks;
+          }
+        }
+        if (!live || (g.first + t) * 128 + 128 > first_end) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (!live || slot >= row_end[r]) s[r] = neg_inf();
+        }
+        if (a.scores != nullptr && slot < g.len && rows_here > 0) {
+          float* to = scores + (long long)slot * a.score_rows;
+          if (a.score_rows >= 4) {
+            *reinterpret_cast<float4*>(to) = make_float4(s[0], s[1], s[2], s[3]);
+            if (a.score_rows == 8) *reinterpret_cast<float4*>(to + 4) = make_float4(s[4], s[5], s[6], s[7]);
+          } else if (a.score_rows == 2) {
+            *reinterpret_cast<float2*>(to) = make_float2(s[0], s[1]);
+          } else {
+            *to = s[0];
+          }
+        }
+        float* mine = my_max + ((x & 1) * 4 + quarter) * 8;
+#pragma unroll
+        for (int r = 0; r < 8; r += 4) {
+          float4 top;
+          top.x = warp_max(s[r] + lv);
+          top.y = warp_max(s[r + 1] + lv);
+          top.z = warp_max(s[r + 2] + lv);
+          top.w = warp_max(s[r + 3] + lv);
+          if (lane == 0) *reinterpret_cast<float4*>(mine + r) = top;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&my_exchange[x & 1]);
+        if (!(ok = warp_wait(&my_exchange[x & 1], (x >> 1) & 1, abort_flag, a.status))) break;
+        // every thread derives the same new references from the four warps' maxima
+        float corr[8];
+        bool moved = false;
+        const float* all = my_max + (x & 1) * 32;
+        ++x;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float top = fmaxf(fmaxf(all[r], all[8 + r]), fmaxf(all[16 + r], all[24 + r]));
+          corr[r] = 1.f;
+          if (top > m[r] + kMaxLead) {
+            corr[r] = ex2_approx(m[r] - top);
+            l[r] *= corr[r];
+            m[r] = top;
+            moved = true;
+          }
+        }
+        if (moved && t > 0) {  // the same on every thread of the group; PV(j - 1) may still add to O
+          if (!(ok = warp_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, a.status))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int hf = 0; hf < C::HALVES; ++hf) {
+            float y[T][8];
+#pragma unroll
+            for (int u = 0; u < T; ++u) tmem_ld8(lane_base + C::COL_O + C::NB * hf + u * R + g8, y[u]);
+#pragma unroll
+            for (int u = 0; u < T; ++u) tmem_ld8_wait(y[u]);
+#pragma unroll
+            for (int u = 0; u < T; ++u) {
+              uint32_t z[8];
+#pragma unroll
+              for (int r = 0; r < 8; ++r) z[r] = __float_as_uint(y[u][r] * corr[r]);
+              tmem_st8(lane_base + C::COL_O + C::NB * hf + u * R + g8, z);
+            }
+          }
+          tmem_st_wait();
+        }
+#pragma unroll
+        for (int r = 0; r < 8; r += 2) {
+          const float p0 = ex2_approx(s[r] - (m[r] == neg_inf() ? 0.f : m[r]));
+          const float p1 = ex2_approx(s[r + 1] - (m[r + 1] == neg_inf() ? 0.f : m[r + 1]));
+          l[r] += p0;
+          l[r + 1] += p1;
+          uint32_t code[T];
+          split_terms<T>(p0 * wv, p1 * wv, code);
+          // 128-byte swizzle: the 16-byte chunk is XORed with the row
+          const uint32_t at = p_row + i * C::P_BYTES + r * 128;
+          const uint32_t c0 = (chunk16 ^ r) << 4, c1 = (chunk16 ^ (r + 1)) << 4;
+#pragma unroll
+          for (int u = 0; u < T; ++u) {
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + c0 + u * R * 128), "r"(code[u] & 0xffu) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + c1 + u * R * 128 + 128), "r"(code[u] >> 8) : "memory");
+          }
+        }
+        if (!live && g8 == 0) {  // no bytes of this slot may reach the product
+          for (int hf = 0; hf < C::HALVES; ++hf) {
+            const int p = j * C::HALVES + hf, at = C::NSK + p % C::NSV;
+            if (!mbar_wait(&ring_full[at], (p / C::NSV) & 1, abort_flag, a.status, kStatusTimeout)) ok = false;
+            uint4* row = reinterpret_cast<uint4*>(sRing + at * C::ITEM + key * C::W);
+            if (ok)
+              for (int c = 0; c < C::W / 16; ++c) row[c] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) mbar_arrive(&p_full[i]);
+      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&seg_free[buf]);
+      // l over the 128 slots of a tile: lanes, then warps
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float y = warp_sum(l[r]);
+        if (lane == 0) my_sum[quarter * 8 + r] = y;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&my_exchange[x & 1]);
+      if (!(ok = warp_wait(&my_exchange[x & 1], (x >> 1) & 1, abort_flag, a.status))) break;
+      ++x;
+      if (!(ok = warp_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, a.status))) break;
+      tc_fence_after();
+      float inv[8];
+      const long long part_row = (long long)g.part * R + g8;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float y = my_sum[r] + my_sum[8 + r] + my_sum[16 + r] + my_sum[24 + r];
+        inv[r] = y == 0.f ? 0.f : (1.f / kWeightScale) / y;
+        if (key == r && r < rows_here) {
+          const float lse2 = y == 0.f ? neg_inf() : (m[r] == neg_inf() ? 0.f : m[r]) + __log2f(y);
+          if (g.part < 0)
+            a.lse[out_row + r] = lse2 * kLn2;
+          else
+            a.lse_part[part_row + r] = lse2;
+        }
+      }
+#pragma unroll
+      for (int hf = 0; hf < C::HALVES; ++hf) {
+        float y[T][8];
+#pragma unroll
+        for (int u = 0; u < T; ++u) tmem_ld8(lane_base + C::COL_O + C::NB * hf + u * R + g8, y[u]);
+#pragma unroll
+        for (int u = 0; u < T; ++u) tmem_ld8_wait(y[u]);
+        const int f = hf * 128 + key;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          float z = y[T - 1][r];
+#pragma unroll
+          for (int u = T - 2; u >= 0; --u) z = fmaf(z, 0.0625f, y[u][r]);
+          z *= inv[r];
+          if (r < rows_here && f < D) {
+            if (g.part >= 0) {
+              a.o_part[(part_row + r) * D + f] = z;
+            } else if (a.bf16) {
+              static_cast<__nv_bfloat16*>(a.o)[(out_row + r) * D + f] = __float2bfloat16_rn(z);
+            } else {
+              static_cast<__half*>(a.o)[(out_row + r) * D + f] = __float2half_rn(z);
             }
           }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 4 * G + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
-// Merges the chunks of a row: LSE = log2 sum 2^LSE_s, O = sum 2^(LSE_s - LSE) O_s,
-// in the chunks' order (GROUPS of threads take every GROUPS-th chunk, then
-// their sums are added in order).
-template <int D>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restrict__ o_part,
-                                                            const float* __restrict__ lse_part,
-                                                            const int* __restrict__ lens, void* __restrict__ o,
-                                                            float* __restrict__ lse, int rows_per_seq,
-                                                            long long rows_all, int splits, int chunk, int max_len,
-                                                            bool bf16) {
-  constexpr int PER = D / 4, GROUPS = 256 / PER;
-  __shared__ float s_w[1024];
-  __shared__ float4 s_o[GROUPS][PER];
-  __shared__ float s_red[8];
-  const long long row = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch();
-  pdl_wait();
-  int len = lens[row / rows_per_seq];
-  if (len < 0 || len > max_len) len = 0;
-  const int ns = (len + chunk - 1) / chunk;  // chunks that hold something
-  float mx = neg_inf();
-  for (int s = threadIdx.x; s < ns; s += 256) {
-    const float x = lse_part[s * rows_all + row];
-    s_w[s] = x;
-    mx = fmaxf(mx, x);  // a NaN reaches the output through its weight
+// Where the parts of a head are: part `first` of the CTA in which it begins,
+// then parts first + 1, first + 3, ... of the next ones (balanced), or parts
+// first, first + 2, ... of its chunks.  `count` parts; 1: it was not shared,
+// 0: it is empty.
+struct Parts {
+  int count;
+  long long first;
+  int jump;  // from the first to the second
+  __device__ __forceinline__ long long at(int s) const { return s == 0 ? first : first + jump + 2 * (s - 1); }
+};
+__device__ __forceinline__ Parts find_parts(const PagedAttnArgs& a, int bh, int tile_y) {
+  const int tb = (good_len(a.lens[bh / a.c.Hkv], a.max_len) + 127) >> 7;
+  Parts p;
+  if (a.balanced) {
+    const int2 x = a.shared[bh];  // written only for heads that hold something
+    p.count = tb > 0 ? x.x : 0;
+    p.first = 2 * ((long long)tile_y * a.ctas + x.y) + 1;
+    p.jump = 1;
+  } else {
+    p.count = (tb + a.per - 1) / a.per;
+    p.first = 2 * ((long long)tile_y * a.ctas + (long long)bh * a.splits);
+    p.jump = 2;
   }
-  mx = warp_max(mx);
-  if (lane == 0) s_red[warp] = mx;
-  __syncthreads();
+  return p;
+}
+
+// sum[k] += sum over the rows, in order, of 2^(score - z[row]) for slots slot0 + 256 k; z = +inf: a row that sees
+// nothing (its scores are -inf).  W rows lie together, groups of W `stride` apart.
+template <int W, int SLOTS>
+__device__ __forceinline__ void add_weights(const float* from, long long stride, const float* z, int rows, int slot0,
+                                            int len, float (&sum)[SLOTS]) {
+  for (int g = 0; g < rows; g += W, from += stride) {
+    float y[SLOTS][W], ref[W];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) mx = fmaxf(mx, s_red[w]);
-  const float ref = mx == neg_inf() ? 0.f : mx;
-  const int g = threadIdx.x / PER, f = threadIdx.x % PER;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int s = g; s < ns; s += GROUPS) {
-    const float w = exp2f(s_w[s] - ref);
-    const float4 x = *reinterpret_cast<const float4*>(o_part + (s * rows_all + row) * D + 4 * f);
-    sum += w;
-    if (w != 0.f) {
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
-    }
-  }
-  s_o[g][f] = acc;
-  __syncthreads();
-  if (f == 0) s_w[g] = sum;  // the weights are no longer needed
-  __syncthreads();
-  if (g == 0) {
-    float l = 0.f;
+    for (int k = 0; k < SLOTS; ++k)
+      if (slot0 + 256 * k < len) {
+        const float* at = from + (long long)(slot0 + 256 * k) * W;
+        if constexpr (W >= 4) {
 #pragma unroll
-    for (int k = 0; k < GROUPS; ++k) l += s_w[k];
+          for (int r = 0; r < W; r += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(at + r);
+            y[k][r] = v.x, y[k][r + 1] = v.y, y[k][r + 2] = v.z, y[k][r + 3] = v.w;
+          }
+        } else if constexpr (W == 2) {
+          const float2 v = *reinterpret_cast<const float2*>(at);
+          y[k][0] = v.x, y[k][1] = v.y;
+        } else {
+          y[k][0] = *at;
+        }
+      }
 #pragma unroll
-    for (int k = 1; k < GROUPS; ++k) {
-      const float4 x = s_o[k][f];
-      acc.x += x.x;
-      acc.y += x.y;
-      acc.z += x.z;
-      acc.w += x.w;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint2 two;
-    if (bf16) {
-      __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-      __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-      two = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-    } else {
-      __half2 lo = __floats2half2_rn(acc.x * inv, acc.y * inv);
-      __half2 hi = __floats2half2_rn(acc.z * inv, acc.w * inv);
-      two = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-    }
-    reinterpret_cast<uint2*>(o)[row * PER + f] = two;
-    if (f == 0) lse[row] = l == 0.f ? neg_inf() : (ref + __log2f(l)) * kLn2;
+    for (int r = 0; r < W; ++r) ref[r] = g + r < rows ? z[g + r] : __int_as_float(0x7f800000);
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k)
+#pragma unroll
+      for (int r = 0; r < W; ++r)
+        if (g + r < rows) sum[k] += ex2_approx(y[k][r] - ref[r]);
   }
 }
 
-// weight_acc[slot] += sum over the rows of 2^(score - LSE), in the rows'
-// order: four slots a thread.
-__global__ void __launch_bounds__(256) paged_weights_kernel(const float* __restrict__ scores,
-                                                            const float* __restrict__ lse,
-                                                            const int* __restrict__ lens,
-                                                            float* __restrict__ weight_acc, int Hkv, int rows,
-                                                            long long score_stride, long long acc_stride,
-                                                            int max_len) {
-  const int bh = blockIdx.y;
-  const int slot = (blockIdx.x * 256 + threadIdx.x) * 4;
-  pdl_wait();
-  const int len = lens[bh / Hkv];
-  if (len > max_len || slot >= len) return;
-  const float* from = scores + (long long)bh * rows * score_stride + slot;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int r = 0; r < rows; ++r) {
-    const float z = lse[(long long)bh * rows + r] * kLog2e;
-    const float4 x = *reinterpret_cast<const float4*>(from + r * score_stride);
-    if (z == neg_inf()) continue;  // the row sees nothing
-    sum[0] += exp2f(x.x - z);
-    sum[1] += exp2f(x.y - z);
-    sum[2] += exp2f(x.z - z);
-    sum[3] += exp2f(x.w - z);
-  }
-  float* to = weight_acc + (long long)bh * acc_stride + slot;
+// Joins the parts of a row that several CTAs shared (the first row_blocks
+// blocks; `team` warps a row): O = sum 2^(LSE_s) O_s / sum 2^(LSE_s), LSE =
+// log2 of that sum, with a running maximum; the warps of a team take parts in
+// turn and are added in order at the end, so the result does not depend on
+// which CTA was first.  Rows of heads that one CTA had alone are in place
+// already; empty sequences get O = 0 and LSE = -inf here.
+// The other blocks add the weights: weight_acc[slot] += sum over the head's
+// rows, in order, of 2^(score - LSE).  LSE is joined from the parts there as
+// well: a launch that waited for the first blocks would take longer.
+template <int D>
+__global__ void __launch_bounds__(256) paged_finish_kernel(const __grid_constant__ PagedAttnArgs a, int row_blocks,
+                                                           int team) {
+  constexpr int V = D / 32;  // features a lane
+  __shared__ float s_o[8][D];
+  __shared__ float2 s_ml[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((int)blockIdx.x < row_blocks) {
+    const int row = blockIdx.x * (8 / team) + warp / team, member = warp % team;
+    const bool there = row < a.c.B * a.c.Hkv * a.rows;
+    const int bh = there ? row / a.rows : 0, in_head = row % a.rows;
+    pdl_wait();
+    const Parts p = find_parts(a, bh, in_head / a.row_tile);
+    float acc[V];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (slot + k < len) to[k] += sum[k];
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    float m = neg_inf(), l = 0.f;
+    const bool mine = there && p.count != 1;
+    if (mine) {
+#pragma unroll 4
+      for (int s = member; s < p.count; s += team) {
+        const long long at = p.at(s) * a.row_tile + in_head % a.row_tile;
+        const float z = a.lse_part[at];
+        float x[V];
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          const float2 two = *reinterpret_cast<const float2*>(a.o_part + at * D + lane * V + i);
+          x[i] = two.x;
+          x[i + 1] = two.y;
+        }
+        const float top = fmaxf(m, z), ref = top == neg_inf() ? 0.f : top;
+        const float c = exp2f(m - ref), w = exp2f(z - ref);
+        m = top;
+        l = l * c + w;
+        // a part that saw nothing has weight 0; a NaN goes through
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = acc[i] * c + (w == 0.f ? 0.f : w * x[i]);
+      }
+    }
+    if (team > 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = acc[i];
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (member == 0) {
+        float top = m;
+        for (int k = 1; k < team; ++k) top = fmaxf(top, s_ml[warp + k].x);
+        const float ref = top == neg_inf() ? 0.f : top;
+        float c = exp2f(m - ref);
+        l *= c;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= c;
+        for (int k = 1; k < team; ++k) {
+          c = exp2f(s_ml[warp + k].x - ref);
+          l += s_ml[warp + k].y * c;
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += s_o[warp + k][lane * V + i] * c;
+        }
+        m = top;
+      }
+    }
+    if (!mine || member != 0) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t out[V / 2];
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      if (a.bf16) {
+        __nv_bfloat162 x = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+        out[i / 2] = *reinterpret_cast<uint32_t*>(&x);
+      } else {
+        __half2 x = __floats2half2_rn(acc[i] * inv, acc[i + 1] * inv);
+        out[i / 2] = *reinterpret_cast<uint32_t*>(&x);
+      }
+    }
+    uint32_t* o = reinterpret_cast<uint32_t*>(a.o) + ((long long)row * D + lane * V) / 2;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) o[i] = out[i];
+    if (lane == 0) a.lse[row] = l == 0.f ? neg_inf() : ((m == neg_inf() ? 0.f : m) + __log2f(l)) * kLn2;
+    return;
+  }
+  // ---------------------------------------------------------------- weights
+  constexpr int SLOTS = 4;   // slots a thread, 256 apart
+  __shared__ float s_z[64];  // LSE of the rows at hand
+  const int per_head = (a.max_len + 256 * SLOTS - 1) / (256 * SLOTS);
+  const int x = blockIdx.x - row_blocks;
+  const int bh = x / per_head, slot0 = (x % per_head) * (256 * SLOTS) + threadIdx.x;
+  pdl_wait();
+  const int len = good_len(a.lens[bh / a.c.Hkv], a.max_len);
+  if ((x % per_head) * (256 * SLOTS) >= len) return;
+  const Parts p = find_parts(a, bh, 0);  // the same for every row tile, but for the first part's number
+  float* to = a.weight_acc + (long long)bh * a.c.width * a.c.ps;
+  float was[SLOTS], sum[SLOTS];
+#pragma unroll
+  for (int k = 0; k < SLOTS; ++k) {
+    was[k] = slot0 + 256 * k < len ? to[slot0 + 256 * k] : 0.f;
+    sum[k] = 0.f;
+  }
+  for (int r0 = 0; r0 < a.rows; r0 += 64) {
+    const int rows = min(64, a.rows - r0);
+    if (r0 > 0) __syncthreads();
+    for (int r = warp; r < rows; r += 8) {  // a warp a row, its lanes the parts
+      const int in_head = r0 + r;
+      float m = neg_inf(), l = 0.f;
+      if (p.count == 1) {
+        m = a.lse[(long long)bh * a.rows + in_head] * kLog2e;
+        l = m == neg_inf() ? 0.f : 1.f;
+      } else {
+        const long long tile = 2ll * (in_head / a.row_tile) * a.ctas;
+        for (int s = lane; s < p.count; s += 32) {
+          const float y = a.lse_part[(tile + p.at(s)) * a.row_tile + in_head % a.row_tile];
+          const float top = fmaxf(m, y), ref = top == neg_inf() ? 0.f : top;
+          l = l * exp2f(m - ref) + exp2f(y - ref);
+          m = top;
+        }
+        const float top = warp_max(m), ref = top == neg_inf() ? 0.f : top;
+        l = warp_sum(l * exp2f(m - ref));
+        m = top;
+      }
+      if (lane == 0) s_z[r] = l == 0.f ? -neg_inf() : (m == neg_inf() ? 0.f : m) + __log2f(l);
+    }
+    __syncthreads();
+    const float* from = a.scores + ((long long)bh * a.score_groups + r0 / 8) * a.score_stride;
+    if (a.score_rows == 1) add_weights<1, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
+    else if (a.score_rows == 2) add_weights<2, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
+    else if (a.score_rows == 4) add_weights<4, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
+    else add_weights<8, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
+  }
+#pragma unroll
+  for (int k = 0; k < SLOTS; ++k)
+    if (slot0 + 256 * k < len) to[slot0 + 256 * k] = was[k] + sum[k];
 }
 
 template <typename... Params, typename... Args>
@@ -779,83 +1145,92 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStr
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
-template <int D, int T, int R>
+template <int D, int T, int G>
 cudaError_t launch_attention_t(const PagedAttnArgs& a, cudaStream_t stream) {
-  using C = PagedCfg<D, T, R>;
-  auto kern = paged_attention_kernel<D, T, R>;
-  const int smem = C::smem((a.chunk + a.c.ps - 1) / a.c.ps);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::smem(kPagedMaxPagesPerChunk));
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.c.B * a.c.Hkv) * (unsigned)a.splits, (unsigned)((a.rows + R - 1) / R));
-  kern<<<grid, C::THREADS, smem, stream>>>(a);
+  using C = PagedCfg<D, T, G>;
+  auto kern = paged_attention_kernel<D, T, G>;
+  const int smem = C::smem(a.seg_pages);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 grid((unsigned)a.ctas, (unsigned)((a.rows + C::R - 1) / C::R));
+  kern<<<grid, C::WARPS * 32, smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <int D, int T>
+cudaError_t launch_groups(const PagedAttnArgs& a, cudaStream_t stream) {
+  switch (a.row_tile) {
+    case 8: return launch_attention_t<D, T, 1>(a, stream);
+    case 16: return launch_attention_t<D, T, 2>(a, stream);
+    case 24: return launch_attention_t<D, T, 3>(a, stream);
+    case 32: return launch_attention_t<D, T, 4>(a, stream);
+    case 40: return launch_attention_t<D, T, 5>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 template <int D>
 cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t stream) {
-  const int r = paged_row_tile(a.rows);
-  cudaError_t e;
-  if (a.bf16)
-    e = r == 8    ? launch_attention_t<D, 2, 8>(a, stream)
-        : r == 16 ? launch_attention_t<D, 2, 16>(a, stream)
-                  : launch_attention_t<D, 2, 32>(a, stream);
-  else
-    e = r == 8    ? launch_attention_t<D, 3, 8>(a, stream)
-        : r == 16 ? launch_attention_t<D, 3, 16>(a, stream)
-                  : launch_attention_t<D, 3, 32>(a, stream);
+  cudaError_t e = a.bf16 ? launch_groups<D, 2>(a, stream) : launch_groups<D, 3>(a, stream);
   if (e != cudaSuccess) return e;
-  const int BH = a.c.B * a.c.Hkv;
-  const long long rows_all = (long long)BH * a.rows;
-  if (a.splits > 1) {
-    e = launch_pdl(paged_combine_kernel<D>, dim3((unsigned)rows_all), dim3(256), stream, a.o_part, a.lse_part, a.lens,
-                   a.o, a.lse, a.c.Hkv * a.rows, rows_all, a.splits, a.chunk, a.max_len, a.bf16);
-    if (e != cudaSuccess) return e;
-  }
-  if (a.weight_acc != nullptr)
-    e = launch_pdl(paged_weights_kernel, dim3((unsigned)((a.max_len + 1023) / 1024), (unsigned)BH), dim3(256), stream,
-                   a.scores, a.lse, a.lens, a.weight_acc, a.c.Hkv, a.rows, a.score_stride,
-                   (long long)a.c.width * a.c.ps, a.max_len);
-  return e;
+  const long long BH = (long long)a.c.B * a.c.Hkv;
+  const bool join = a.balanced || a.splits > 1;
+  // warps that join a row: about as many as it has parts
+  int team = 1;
+  if (a.balanced)
+    while (team < 8 && team * BH < a.ctas) team *= 2;
+  else
+    while (team < 8 && team < a.splits) team *= 2;
+  const long long row_blocks = join ? (BH * a.rows * team + 7) / 8 : 0;
+  const long long blocks = row_blocks + (a.weight_acc ? BH * ((a.max_len + 1023) / 1024) : 0);
+  if (blocks == 0) return cudaSuccess;
+  return launch_pdl(paged_finish_kernel<D>, dim3((unsigned)blocks), dim3(256), stream, a, (int)row_blocks, team);
 }
 
 }  // namespace
 
-int paged_row_tile(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
-
-void paged_plan(int BH, int rows, int ps, int max_len, int num_splits, int* splits, int* chunk) {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int r = paged_row_tile(rows);
-  const long long resident = 2LL * sms;
-  const long long units = (long long)BH * ((rows + r - 1) / r);
+PagedPlan paged_plan(int B, int Hkv, int rows, int d, int ps, int max_len, int num_splits) {
+  PagedPlan p;
+  // row tiles of at most 40 rows, as even as groups of eight allow
+  const int row_tiles = (rows + 39) / 40;
+  p.row_tile = ((rows + row_tiles - 1) / row_tiles + 7) / 8 * 8;
+  const int sms = sm_count();
+  const long long resident = (p.row_tile == 8 && d <= 128 ? 2LL : 1LL) * sms;
+  const long long BH = (long long)B * Hkv;
   const int tiles = (max_len + 127) / 128;
-  const int most = kPagedMaxPagesPerChunk * ps;
-  const int most_tiles = (most < kPagedMaxChunk ? most : kPagedMaxChunk) / 128;
-  int best_per = 1;
-  if (num_splits > 0) {
-    best_per = (tiles + num_splits - 1) / num_splits;
+  const long long all = BH * places_of(tiles);
+  constexpr int kMostTiles = kPagedMaxChunk / 128;
+  p.min_tiles = 4;
+  int segment;  // tiles of the longest segment
+  if (num_splits == 0 && tiles > 4 && B <= kPagedMaxBalanced) {
+    // The device shares out what there is.  A CTA never gets more than
+    // kMostTiles, whatever the lengths are.
+    p.balanced = true;
+    long long ctas = resident / row_tiles;
+    if (ctas < 1) ctas = 1;
+    const long long want = (all + p.min_tiles - 1) / p.min_tiles, need = (all + kMostTiles - 2) / (kMostTiles - 1);
+    if (ctas > want) ctas = want;
+    if (ctas < need) ctas = need;
+    p.ctas = ctas;
+    p.splits = 1;
+    p.per = 0;
+    const long long share = (all + ctas - 1) / ctas + 1;
+    segment = (int)(share < tiles ? share : tiles);
+    p.parts = 2 * ctas * row_tiles;
   } else {
-    // waves of CTAs, each as long as its tiles and about three more for its
-    // start and end; several chunks cost the merge's launch, about four
-    double best = 1e300;
-    const int most_splits = tiles < 1024 ? tiles : 1024;
-    for (int s = 1; s <= most_splits; ++s) {
-      const int per = (tiles + s - 1) / s;
-      if (per > most_tiles) continue;
-      const int got = (tiles + per - 1) / per;
-      const double waves = (double)((units * got + resident - 1) / resident);
-      const double cost = waves * (per + 3.0) + (got > 1 ? 4.0 : 0.0) + 0.02 * got;
-      if (cost < best) {
-        best = cost;
-        best_per = per;
-      }
-    }
+    const int splits = num_splits ? num_splits : 1;
+    p.balanced = false;
+    p.per = (tiles + splits - 1) / splits;
+    if (p.per > kMostTiles) p.per = kMostTiles;
+    p.splits = (tiles + p.per - 1) / p.per;
+    p.ctas = BH * p.splits;
+    segment = p.per;
+    p.parts = p.splits > 1 ? 2 * p.ctas * row_tiles : 0;
   }
-  if (best_per > most_tiles) best_per = most_tiles;
-  if (best_per < 1) best_per = 1;
-  *chunk = best_per * 128;
-  *splits = (tiles + best_per - 1) / best_per;
+  p.seg_pages = (segment * 128 + ps - 1) / ps;
+  return p;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream) {

@@ -19,11 +19,26 @@ struct PagedView {
   bool e5m2 = false;
 };
 
-// Pages one CTA of the attention kernel can list (its share of the table
-// sits in shared memory), and slots of a chunk (what can be lost of tiny
-// weights grows with it): bounds of a chunk.
-constexpr int kPagedMaxPagesPerChunk = 1024;
+// Slots of one segment of attention: what can be lost of tiny weights grows
+// with it, and its page list sits in shared memory.
 constexpr int kPagedMaxChunk = 16384;
+// Sequences whose lengths every CTA adds up to find its share.
+constexpr int kPagedMaxBalanced = 1024;
+// Parts that a row can have (the chunks of a head, or the CTAs that share it)
+// and the slots that this allows at 127 tiles a part.
+constexpr int kPagedMaxParts = 4096;
+constexpr int kPagedMaxSlots = (kPagedMaxParts - 2) * 127 * 128;
+
+// How the tiles are shared out among CTAs (see fa_paged.cu).
+struct PagedPlan {
+  int row_tile = 8;        // query rows of a CTA
+  bool balanced = false;   // by the lengths, on the device; else `splits` chunks of `per` tiles a head
+  long long ctas = 1;      // CTAs a row tile
+  int splits = 1, per = 1;
+  int min_tiles = 1;       // balanced: places on the line of heads that are worth a CTA
+  int seg_pages = 1;       // pages of the longest segment
+  long long parts = 0;     // partial results in the workspace, row_tile rows each
+};
 
 struct PagedAttnArgs {
   CUtensorMap tm_k, tm_v;    // [pages * Hkv, ps, d] bytes, box one page (of 128 or 64 bytes a row)
@@ -32,21 +47,22 @@ struct PagedAttnArgs {
   const int* lens;           // [B]
   void* o;                   // [B, Hkv, rows, d] 16 bit
   float* lse;                // [B, Hkv, rows]
-  float* o_part;             // [splits, B * Hkv, rows, d] (splits > 1)
-  float* lse_part;           // [splits, B * Hkv, rows], log2 units
-  float* scores;             // [B * Hkv, rows, score_stride], log2 units, or null
+  float* o_part;             // [parts, row_tile, d]
+  float* lse_part;           // [parts, row_tile], log2 units
+  int2* shared;              // [B * Hkv]: CTAs that share the head, the first of them (balanced)
+  float* scores;             // [B * Hkv, score_groups, slots, score_rows], log2 units, or null
   float* weight_acc;         // [B * Hkv, width * ps], or null
   int rows, Nq;              // query rows of a K / V head, rows = group * Nq, row R is query R % Nq
-  int max_len, splits, chunk;
-  long long score_stride;
+  int max_len;
+  int row_tile, ctas, splits, per, min_tiles, seg_pages;  // the plan
+  bool balanced;
+  int score_rows, score_groups;    // rows of a group (1, 2, 4 or 8) and groups of a head
+  long long score_stride;          // floats of a group
   bool causal, bf16;
   float scale_log2;
   unsigned int* status;
 };
-// Rows of one CTA for `rows` query rows of a head.
-int paged_row_tile(int rows);
-// The chunk (a multiple of 128 slots) and the number of chunks of max_len slots.
-void paged_plan(int BH, int rows, int ps, int max_len, int num_splits, int* splits, int* chunk);
+PagedPlan paged_plan(int B, int Hkv, int rows, int d, int ps, int max_len, int num_splits);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream);
 
 struct PagedAppendArgs {
@@ -83,6 +99,7 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream);
 
 // Shared by the entry points (fa_api.cu).
 unsigned int* device_status_word();
+int sm_count();  // of the current device
 bool encode_tiled_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const cuuint64_t (&dims)[3],
                       const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle);
 

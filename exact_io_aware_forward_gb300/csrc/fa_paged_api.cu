@@ -2,6 +2,7 @@
 // and workspace layout.  Nothing is allocated here.
 #include <math.h>
 #include <stdint.h>
+#include <vector_types.h>
 
 #include "../../include/fa_gb300.h"
 #include "fa_paged.h"
@@ -56,10 +57,12 @@ bool overlap(const void* x, const void* y, long long n) {
 }
 
 struct AttnPlan {
-  int rows = 0, max_len = 0, splits = 1, chunk = 0;
+  int rows = 0, max_len = 0;
+  fa::PagedPlan share;
+  int score_rows = 1, score_groups = 1;
   long long score_stride = 0;
-  size_t o_part = 0, lse_part = 0, scores = 0;  // bytes
-  size_t total() const { return o_part + lse_part + scores; }
+  size_t o_part = 0, lse_part = 0, shared = 0, scores = 0;  // bytes
+  size_t total() const { return o_part + lse_part + shared + scores; }
 };
 
 fa_status attention_plan(const fa_paged_cache* c, int Hq, int Nq, int max_len, int num_splits, bool weights,
@@ -72,14 +75,18 @@ fa_status attention_plan(const fa_paged_cache* c, int Hq, int Nq, int max_len, i
   if (rows > 65535 * 8LL || BH * rows * c->d >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   p->rows = (int)rows;
   p->max_len = max_len ? max_len : slots;
-  fa::paged_plan((int)BH, p->rows, c->page_size, p->max_len, num_splits, &p->splits, &p->chunk);
-  if (p->splits > 1024 || BH * p->splits >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
-  if (p->splits > 1) {
-    p->o_part = align256((size_t)p->splits * BH * rows * c->d * sizeof(float));
-    p->lse_part = align256((size_t)p->splits * BH * rows * sizeof(float));
-  }
-  p->score_stride = (p->max_len + 3LL) / 4 * 4;
-  if (weights) p->scores = align256((size_t)BH * rows * p->score_stride * sizeof(float));
+  if (p->max_len > fa::kPagedMaxSlots) return FA_ERR_UNSUPPORTED;
+  p->share = fa::paged_plan(c->B, c->Hkv, p->rows, c->d, c->page_size, p->max_len, num_splits);
+  if (BH * rows + BH * ((p->max_len + 1023) / 1024) >= (1LL << 31)) return FA_ERR_UNSUPPORTED;  // blocks of the join
+  if (p->share.ctas >= (1LL << 31) || p->share.parts >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  const size_t part_rows = (size_t)p->share.parts * p->share.row_tile;
+  p->o_part = align256(part_rows * c->d * sizeof(float));
+  p->lse_part = align256(part_rows * sizeof(float));
+  if (p->share.balanced) p->shared = align256((size_t)BH * sizeof(int2));
+  p->score_rows = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
+  p->score_groups = (int)((rows + 7) / 8);
+  p->score_stride = (long long)p->max_len * p->score_rows;
+  if (weights) p->scores = align256((size_t)BH * p->score_groups * p->score_stride * sizeof(float) );
   return FA_OK;
 }
 
@@ -166,8 +173,15 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const void* q, const int
   a.rows = p.rows;
   a.Nq = Nq;
   a.max_len = p.max_len;
-  a.splits = p.splits;
-  a.chunk = p.chunk;
+  a.row_tile = p.share.row_tile;
+  a.ctas = (int)p.share.ctas;
+  a.splits = p.share.splits;
+  a.per = p.share.per;
+  a.min_tiles = p.share.min_tiles;
+  a.seg_pages = p.share.seg_pages;
+  a.balanced = p.share.balanced;
+  a.score_rows = p.score_rows;
+  a.score_groups = p.score_groups;
   a.score_stride = p.score_stride;
   a.causal = causal != 0;
   a.bf16 = dtype == FA_BF16;
@@ -175,7 +189,8 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const void* q, const int
   char* ws = static_cast<char*>(workspace);
   a.o_part = reinterpret_cast<float*>(ws);
   a.lse_part = reinterpret_cast<float*>(ws + p.o_part);
-  a.scores = weight_acc ? reinterpret_cast<float*>(ws + p.o_part + p.lse_part) : nullptr;
+  a.shared = reinterpret_cast<int2*>(ws + p.o_part + p.lse_part);
+  a.scores = weight_acc ? reinterpret_cast<float*>(ws + p.o_part + p.lse_part + p.shared) : nullptr;
   a.status = fa::device_status_word();
   if (!a.status) return FA_ERR_CUDA;
   return fa::launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -464,12 +464,16 @@ fa_status fa_paged_append(const fa_paged_cache* cache, const void* k, const void
  * that share its head.
  * weight_acc (or NULL): the weight exp(S - LSE) of every seen slot, summed over
  * the Nq queries of the query heads that share the K / V head, is added.
- * max_len (host int, 0 for pages_per_seq * page_size): bounds the lengths and
- * sizes the grid.  num_splits: chunks of max_len, 0 picks; at most 1024.
+ * max_len (host int, 0 for pages_per_seq * page_size; at most 66552064): bounds the
+ * lengths and sizes the grid.  num_splits = 0: the slots that there are (by
+ * the lengths on the device) are shared out evenly among the GPU's SMs; the
+ * places where a sequence's slots are cut then depend on the other lengths of the batch.
+ * num_splits in 1 .. 1024: every head's max_len slots are cut into so many chunks (of at
+ * most 16384 slots: more of them if needed), and a sequence's results are bit for
+ * bit the same in every batch.
  * workspace: fa_paged_workspace_size(cache, Hq, Nq, max_len, num_splits,
  * weight_acc != NULL) bytes, 256-byte aligned, contents irrelevant on entry;
- * calls that overlap on the GPU need one each.  The size is 0 for invalid
- * arguments only.
+ * calls that overlap on the GPU need one each.  0 for invalid arguments.
  * Arithmetic: scores and sums in float32; a query's elements and the softmax
  * weights enter the 8-bit tensor-core products as sums of e4m3 terms
  * that hold the 8 (FA_BF16) or 11 (FA_FP16) bits of the 16-bit type.  Results

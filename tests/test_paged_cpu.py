@@ -93,19 +93,35 @@ def test_bad_evict_arguments(lib, kw, want):
 
 
 def test_workspace_sizes(lib):
+    """O and LSE of two parts a CTA, 8 G rows each; scores of every row and slot for the weights."""
     size = lib.fa_paged_workspace_size
-    # one chunk: nothing to merge; chunks of 128 slots: O and LSE of each
-    assert size(cache(), 8, 1, 0, 1, 0) == 256
-    rows = 2 * 8 * 3
-    assert size(cache(), 8, 3, 512, 4, 0) == 4 * rows * 128 * 4 + 4 * rows * 4
-    assert size(cache(), 8, 3, 512, 4, 1) == 4 * rows * 128 * 4 + 4 * rows * 4 + rows * 512 * 4
+
+    def parts(n, rows, d=128):
+        return n * rows * d * 4 + (n * rows * 4 + 255) // 256 * 256
+
+    # one chunk, or at most 512 slots: nothing to merge
+    assert size(cache(), 8, 1, 0, 1, 0) == 256 and size(cache(), 8, 1, 512, 0, 0) == 256
+    # 2 x 4 heads, 6 rows (a tile of 8), four chunks
+    assert size(cache(), 8, 3, 512, 4, 0) == parts(2 * 8 * 4, 8)
+    assert size(cache(), 8, 3, 512, 4, 1) == parts(2 * 8 * 4, 8) + 8 * 8 * 512 * 4
+    assert size(cache(), 4, 3, 512, 4, 1) == parts(2 * 8 * 4, 8) + 8 * 4 * 512 * 4
+    # 50 rows: two tiles of 32
+    assert size(cache(), 8, 25, 512, 2, 0) == parts(2 * 8 * 2 * 2, 32)
     # a count that leaves a last chunk empty is lowered
-    assert size(cache(), 8, 1, 300, 1000, 0) == 3 * 16 * 128 * 4 + 256
-    # a chunk has at most 16384 slots, and 1024 pages
+    assert size(cache(), 8, 1, 300, 1000, 0) == parts(2 * 8 * 3, 8)
+    # a chunk has at most 16384 slots
     big = cache(pages_per_seq=1 << 11, num_pages=1 << 12)
-    assert size(big, 8, 1, 0, 1, 0) == 8 * 16 * 128 * 4 + 512
-    small = cache(page_size=16, pages_per_seq=1 << 12)
-    assert size(small, 8, 1, 0, 1, 0) == 4 * 16 * 128 * 4 + 256
+    assert size(big, 8, 1, 0, 1, 0) == parts(2 * 8 * 8, 8)
+    # shared out evenly: a CTA for a head's start and two tiles at least, no more CTAs than fit (152 SMs without a GPU) ...
+    mid = cache(pages_per_seq=16)
+    assert size(mid, 8, 1, 0, 0, 0) == parts(2 * 8 * (8 + 2) // 4, 8) + 256
+    assert size(big, 8, 1, 0, 0, 0) == parts(2 * 304, 8) + 256
+    assert size(big, 80, 2, 0, 0, 0) == parts(2 * 152, 40) + 256
+    # ... unless one would get more than 127 tiles
+    huge = cache(pages_per_seq=1 << 15, num_pages=1 << 17)
+    assert size(huge, 8, 1, 0, 0, 0) == parts(2 * -(-8 * ((1 << 14) + 2) // 127), 8) + 256
+    # slots that cannot be merged
+    assert size(cache(pages_per_seq=1 << 20, num_pages=1 << 21), 8, 1, 0, 0, 0) == 0
     ev = lib.fa_paged_evict_workspace_size
     assert ev(cache(), 100) == 256 + 2 * 3328 + 6400 and ev(cache(), 0) == 0 and ev(cache(), 513) == 0
 

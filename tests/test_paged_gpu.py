@@ -63,6 +63,51 @@ def test_attention_matches_oracle(case, weights):
     check_attention(qf, c, lens, 1 / math.sqrt(d), causal, dtype, o, lse, acc, added=2.5)
 
 
+SHARED = [  # B, Hq, Hkv, Nq, d, longest, ps, dtype, kind: many sequences, several a CTA
+    (40, 16, 8, 1, 128, 900, 16, "bf16", "e4m3"),
+    (1000, 2, 2, 1, 64, 120, 64, "bf16", "e4m3"),       # one tile each
+    (300, 4, 2, 2, 64, 260, 32, "fp16", "e5m2"),
+    (90, 4, 2, 10, 128, 500, 128, "bf16", "e4m3"),       # 20 rows: three groups
+    (30, 10, 2, 8, 256, 700, 32, "fp16", "e4m3"),        # 40 rows: five groups
+    (30, 12, 2, 8, 64, 700, 32, "bf16", "e4m3"),         # 48 rows: two row tiles of 24
+    (1100, 1, 1, 1, 64, 300, 16, "bf16", "e4m3"),        # too many to share out: one head a CTA
+    (3, 4, 2, 1, 128, 4000, 16, "bf16", "e4m3"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_ragged_batches_match_oracle(case):
+    """Lengths of all kinds (a third of them 0, 1, or whole tiles): the CTAs' shares begin and end anywhere."""
+    B, Hq, Hkv, Nq, d, longest, ps, dtype, kind = SHARED[case]
+    rng = np.random.default_rng(200 + case)
+    lens = rng.integers(2, longest + 1, B)
+    odd = rng.integers(0, 3, B) == 0
+    lens[odd] = rng.choice([0, 1, 127, 128, 129, 256], B)[odd]
+    lens = np.minimum(lens, longest)
+    lens[-1], lens[0] = 0, longest
+    T = (longest + ps - 1) // ps
+    c = Cache(B, Hkv, T, ps, d, kind, seed=210 + case)
+    qf, q = _q(B, Hq, Nq, d, dtype, 220 + case)
+    acc = torch.zeros(B, Hkv, T * ps, device="cuda")
+    handle = c.to("cuda")
+    if T * ps <= 512:  # shared out from 513 slots on
+        handle = fa.PagedCache(*c.t[:4], torch.cat([c.t[4], torch.full((B, 512 // ps), -1, dtype=torch.int32,
+                                                                      device="cuda")], 1))
+        acc = torch.zeros(B, Hkv, handle.slots, device="cuda")
+    o, lse = fa.forward_paged(handle, q.cuda(), _lens(lens.tolist()), causal=True, weight_acc=acc)
+    fa.fa_device_status()
+    check_attention(qf, c, lens.tolist(), 1 / math.sqrt(d), True, dtype, o, lse, acc[..., :T * ps], added=0.0)
+    # chunks by num_splits: the same numbers up to rounding, and the same bits whatever the batch is
+    acc1 = torch.zeros_like(acc)
+    o1, lse1 = fa.forward_paged(handle, q.cuda(), _lens(lens.tolist()), causal=True, weight_acc=acc1, num_splits=2)
+    fa.fa_device_status()
+    check_attention(qf, c, lens.tolist(), 1 / math.sqrt(d), True, dtype, o1, lse1, acc1[..., :T * ps], added=0.0)
+    one = fa.PagedCache(*handle.tensors[:4], handle.tensors[4][:1].contiguous())
+    o2, lse2 = fa.forward_paged(one, q[:1].cuda(), _lens(lens[:1].tolist()), causal=True, num_splits=2)
+    fa.fa_device_status()
+    assert torch.equal(o1[:1], o2) and torch.equal(lse1[:1], lse2)
+
+
 def test_scales_far_apart():
     """Pages whose scales differ by 2^40 in K (scores near 0 beside ordinary ones) and by 10^6 in V."""
     c = Cache(2, 2, 9, 64, 128, seed=3)
