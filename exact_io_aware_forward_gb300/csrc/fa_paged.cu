@@ -990,6 +990,9 @@ __device__ __forceinline__ void add_weights(const float* from, long long stride,
   }
 }
 
+// 16 scores a thread under way
+constexpr int weight_slots(int w) { return w == 8 ? 2 : 4; }
+
 // Joins the parts of a row that several CTAs shared (the first row_blocks
 // blocks; `team` warps a row): O = sum 2^(LSE_s) O_s / sum 2^(LSE_s), LSE =
 // log2 of that sum, with a running maximum; the warps of a team take parts in
@@ -999,8 +1002,8 @@ __device__ __forceinline__ void add_weights(const float* from, long long stride,
 // The other blocks add the weights: weight_acc[slot] += sum over the head's
 // rows, in order, of 2^(score - LSE).  LSE is joined from the parts there as
 // well: a launch that waited for the first blocks would take longer.
-template <int D>
-__global__ void __launch_bounds__(256) paged_finish_kernel(const __grid_constant__ PagedAttnArgs a, int row_blocks,
+template <int D, int W>
+__global__ void __launch_bounds__(256, 5) paged_finish_kernel(const __grid_constant__ PagedAttnArgs a, int row_blocks,
                                                            int team) {
   constexpr int V = D / 32;  // features a lane
   __shared__ float s_o[8][D];
@@ -1018,7 +1021,7 @@ __global__ void __launch_bounds__(256) paged_finish_kernel(const __grid_constant
     float m = neg_inf(), l = 0.f;
     const bool mine = there && p.count != 1;
     if (mine) {
-#pragma unroll 4
+#pragma unroll 2
       for (int s = member; s < p.count; s += team) {
         const long long at = p.at(s) * a.row_tile + in_head % a.row_tile;
         const float z = a.lse_part[at];
@@ -1079,56 +1082,55 @@ __global__ void __launch_bounds__(256) paged_finish_kernel(const __grid_constant
     if (lane == 0) a.lse[row] = l == 0.f ? neg_inf() : ((m == neg_inf() ? 0.f : m) + __log2f(l)) * kLn2;
     return;
   }
-  // ---------------------------------------------------------------- weights
-  constexpr int SLOTS = 4;   // slots a thread, 256 apart
-  __shared__ float s_z[64];  // LSE of the rows at hand
-  const int per_head = (a.max_len + 256 * SLOTS - 1) / (256 * SLOTS);
-  const int x = blockIdx.x - row_blocks;
-  const int bh = x / per_head, slot0 = (x % per_head) * (256 * SLOTS) + threadIdx.x;
-  pdl_wait();
-  const int len = good_len(a.lens[bh / a.c.Hkv], a.max_len);
-  if ((x % per_head) * (256 * SLOTS) >= len) return;
-  const Parts p = find_parts(a, bh, 0);  // the same for every row tile, but for the first part's number
-  float* to = a.weight_acc + (long long)bh * a.c.width * a.c.ps;
-  float was[SLOTS], sum[SLOTS];
+  if constexpr (W > 0) {
+    // ---------------------------------------------------------------- weights
+    constexpr int SLOTS = weight_slots(W);  // slots a thread, 256 apart
+    __shared__ float s_z[64];  // LSE of the rows at hand
+    const int per_head = (a.max_len + 256 * SLOTS - 1) / (256 * SLOTS);
+    const int x = blockIdx.x - row_blocks;
+    const int bh = x / per_head, slot0 = (x % per_head) * (256 * SLOTS) + threadIdx.x;
+    pdl_wait();
+    const int len = good_len(a.lens[bh / a.c.Hkv], a.max_len);
+    if ((x % per_head) * (256 * SLOTS) >= len) return;
+    const Parts p = find_parts(a, bh, 0);  // the same for every row tile, but for the first part's number
+    float* to = a.weight_acc + (long long)bh * a.c.width * a.c.ps;
+    float was[SLOTS], sum[SLOTS];
 #pragma unroll
-  for (int k = 0; k < SLOTS; ++k) {
-    was[k] = slot0 + 256 * k < len ? to[slot0 + 256 * k] : 0.f;
-    sum[k] = 0.f;
-  }
-  for (int r0 = 0; r0 < a.rows; r0 += 64) {
-    const int rows = min(64, a.rows - r0);
-    if (r0 > 0) __syncthreads();
-    for (int r = warp; r < rows; r += 8) {  // a warp a row, its lanes the parts
-      const int in_head = r0 + r;
-      float m = neg_inf(), l = 0.f;
-      if (p.count == 1) {
-        m = a.lse[(long long)bh * a.rows + in_head] * kLog2e;
-        l = m == neg_inf() ? 0.f : 1.f;
-      } else {
-        const long long tile = 2ll * (in_head / a.row_tile) * a.ctas;
-        for (int s = lane; s < p.count; s += 32) {
-          const float y = a.lse_part[(tile + p.at(s)) * a.row_tile + in_head % a.row_tile];
-          const float top = fmaxf(m, y), ref = top == neg_inf() ? 0.f : top;
-          l = l * exp2f(m - ref) + exp2f(y - ref);
+    for (int k = 0; k < SLOTS; ++k) {
+      was[k] = slot0 + 256 * k < len ? to[slot0 + 256 * k] : 0.f;
+      sum[k] = 0.f;
+    }
+    for (int r0 = 0; r0 < a.rows; r0 += 64) {
+      const int rows = min(64, a.rows - r0);
+      if (r0 > 0) __syncthreads();
+      for (int r = warp; r < rows; r += 8) {  // a warp a row, its lanes the parts
+        const int in_head = r0 + r;
+        float m = neg_inf(), l = 0.f;
+        if (p.count == 1) {
+          m = a.lse[(long long)bh * a.rows + in_head] * kLog2e;
+          l = m == neg_inf() ? 0.f : 1.f;
+        } else {
+          const long long tile = 2ll * (in_head / a.row_tile) * a.ctas;
+          for (int s = lane; s < p.count; s += 32) {
+            const float y = a.lse_part[(tile + p.at(s)) * a.row_tile + in_head % a.row_tile];
+            const float top = fmaxf(m, y), ref = top == neg_inf() ? 0.f : top;
+            l = l * exp2f(m - ref) + exp2f(y - ref);
+            m = top;
+          }
+          const float top = warp_max(m), ref = top == neg_inf() ? 0.f : top;
+          l = warp_sum(l * exp2f(m - ref));
           m = top;
         }
-        const float top = warp_max(m), ref = top == neg_inf() ? 0.f : top;
-        l = warp_sum(l * exp2f(m - ref));
-        m = top;
+        if (lane == 0) s_z[r] = l == 0.f ? -neg_inf() : (m == neg_inf() ? 0.f : m) + __log2f(l);
       }
-      if (lane == 0) s_z[r] = l == 0.f ? -neg_inf() : (m == neg_inf() ? 0.f : m) + __log2f(l);
+      __syncthreads();
+      const float* from = a.scores + ((long long)bh * a.score_groups + r0 / 8) * a.score_stride;
+      add_weights<W, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
     }
-    __syncthreads();
-    const float* from = a.scores + ((long long)bh * a.score_groups + r0 / 8) * a.score_stride;
-    if (a.score_rows == 1) add_weights<1, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
-    else if (a.score_rows == 2) add_weights<2, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
-    else if (a.score_rows == 4) add_weights<4, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
-    else add_weights<8, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
-  }
 #pragma unroll
-  for (int k = 0; k < SLOTS; ++k)
-    if (slot0 + 256 * k < len) to[slot0 + 256 * k] = was[k] + sum[k];
+    for (int k = 0; k < SLOTS; ++k)
+      if (slot0 + 256 * k < len) to[slot0 + 256 * k] = was[k] + sum[k];
+  }
 }
 
 template <typename... Params, typename... Args>
@@ -1184,9 +1186,16 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t stream) {
   else
     while (team < 8 && team < a.splits) team *= 2;
   const long long row_blocks = join ? (BH * a.rows * team + 7) / 8 : 0;
-  const long long blocks = row_blocks + (a.weight_acc ? BH * ((a.max_len + 1023) / 1024) : 0);
+  const int width = a.weight_acc ? a.score_rows : 0;
+  const int per_block = 256 * weight_slots(width);
+  const long long blocks = row_blocks + (width ? BH * ((a.max_len + per_block - 1) / per_block) : 0);
   if (blocks == 0) return cudaSuccess;
-  return launch_pdl(paged_finish_kernel<D>, dim3((unsigned)blocks), dim3(256), stream, a, (int)row_blocks, team);
+  auto kern = width == 0   ? paged_finish_kernel<D, 0>
+              : width == 1 ? paged_finish_kernel<D, 1>
+              : width == 2 ? paged_finish_kernel<D, 2>
+              : width == 4 ? paged_finish_kernel<D, 4>
+                           : paged_finish_kernel<D, 8>;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), stream, a, (int)row_blocks, team);
 }
 
 }  // namespace

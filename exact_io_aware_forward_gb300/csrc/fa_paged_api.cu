@@ -77,7 +77,7 @@ fa_status attention_plan(const fa_paged_cache* c, int Hq, int Nq, int max_len, i
   p->max_len = max_len ? max_len : slots;
   if (p->max_len > fa::kPagedMaxSlots) return FA_ERR_UNSUPPORTED;
   p->share = fa::paged_plan(c->B, c->Hkv, p->rows, c->d, c->page_size, p->max_len, num_splits);
-  if (BH * rows + BH * ((p->max_len + 1023) / 1024) >= (1LL << 31)) return FA_ERR_UNSUPPORTED;  // blocks of the join
+  if (BH * rows + BH * ((p->max_len + 511) / 512) >= (1LL << 31)) return FA_ERR_UNSUPPORTED;  // blocks of the join
   if (p->share.ctas >= (1LL << 31) || p->share.parts >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   const size_t part_rows = (size_t)p->share.parts * p->share.row_tile;
   p->o_part = align256(part_rows * c->d * sizeof(float));
