@@ -474,6 +474,9 @@ def fa_forward_decode_gqa(q, k, v, o, lse, workspace, causal=False, scale=None, 
 
 
 # ---------------------------------------------------------------- 8-bit paged cache
+# The current stream's handle: torch.cuda.current_stream() makes an object of it first, which takes longer than a launch.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _CACHE_CODE = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 
 
@@ -497,6 +500,7 @@ class PagedCache:
         self.device = k_pages.device
         if any(t.device != self.device for t in self.tensors):
             raise ValueError("the cache's tensors must be on one device")
+        self._index = self.device.index
         self.B, self.pages_per_seq = page_table.shape
         self.num_pages, self.Hkv, self.page_size, self.d = P, Hkv, ps, d
         self.slots = self.pages_per_seq * ps  # a sequence's capacity
@@ -504,10 +508,10 @@ class PagedCache:
         self._ref = ctypes.byref(self._struct)
 
     def _stream(self, stream):
-        """The stream to launch on (current device's by default), with the cache's device current."""
-        if self.device.index != torch.cuda.current_device():
+        """The stream to launch on (the current one by default); the cache's device has to be current."""
+        if torch.cuda.current_device() != self._index:
             raise ValueError(f"the cache is on {self.device}: make it the current device")
-        return ctypes_stream(torch.cuda.current_stream() if stream is None else stream)
+        return _current_stream(self._index) if stream is None else ctypes_stream(stream)
 
     def _tensor(self, name, t, shape, dtype):
         """The pointer of a contiguous tensor on the cache's device."""

@@ -99,9 +99,10 @@ bool page_map(CUtensorMap* m, const void* ptr, const fa_paged_cache* c) {
                               row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-size_t evict_bytes(const fa_paged_cache* c, int keep, size_t* holes, size_t* movers, size_t* scales) {
+size_t evict_bytes(const fa_paged_cache* c, int keep, size_t* pages, size_t* holes, size_t* movers, size_t* scales) {
   const size_t bh = (size_t)c->B * c->Hkv;
-  *holes = align256(bh * sizeof(int));
+  *pages = align256(bh * sizeof(int));
+  *holes = *pages + align256(bh * ((keep + c->page_size - 1) / c->page_size + 1) * sizeof(int));
   *movers = *holes + align256(bh * keep * sizeof(int));
   *scales = *movers + align256(bh * keep * sizeof(int));
   return *scales + align256(bh * keep * 2 * sizeof(float));
@@ -198,8 +199,8 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const void* q, const int
 
 size_t fa_paged_evict_workspace_size(const fa_paged_cache* cache, int keep) {
   if (check_cache(cache) != FA_OK || keep < 1 || keep > cache->pages_per_seq * cache->page_size) return 0;
-  size_t h, m, s;
-  return evict_bytes(cache, keep, &h, &m, &s);
+  size_t p, h, m, s;
+  return evict_bytes(cache, keep, &p, &h, &m, &s);
 }
 
 fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, int* new_lens, float* weight_acc,
@@ -214,8 +215,8 @@ fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, int* new_
   if (!aligned4(lens) || !aligned4(new_lens) || !aligned16(weight_acc) || !aligned16(positions) ||
       overlap(lens, new_lens, cache->B))
     return FA_ERR_INVALID_ARG;
-  size_t h, m, s;
-  const size_t need = evict_bytes(cache, keep, &h, &m, &s);
+  size_t p, h, m, s;
+  const size_t need = evict_bytes(cache, keep, &p, &h, &m, &s);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need) return FA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   a.lens = lens;
@@ -225,6 +226,7 @@ fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, int* new_
   a.keep = keep;
   a.recent = recent;
   a.plan_count = reinterpret_cast<int*>(ws);
+  a.page_holes = reinterpret_cast<int*>(ws + p);
   a.holes = reinterpret_cast<int*>(ws + h);
   a.movers = reinterpret_cast<int*>(ws + m);
   a.mover_scales = reinterpret_cast<float2*>(ws + s);
