@@ -88,12 +88,12 @@ struct PagedEvictArgs {
   float* weight_acc;         // [B, Hkv, width * ps]
   int* positions;            // [B, Hkv, width * ps]
   int keep, recent;
-  // workspace, per (b, h): holes in all and before each page, the holes, the slots that move, and their scales
+  // workspace, per (b, h): holes in all and before each page, the holes, the slots that move
   int* plan_count;           // [B * Hkv]
   int* page_holes;           // [B * Hkv, pages of keep + 1]
   int* holes;                // [B * Hkv, keep]
   int* movers;               // [B * Hkv, keep]
-  float2* mover_scales;      // [B * Hkv, keep] (K, V)
+  float2* edge_scales;       // [B * Hkv] (K, V) of the page where the kept part ends
   unsigned int* status;
 };
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream);

@@ -105,7 +105,7 @@ size_t evict_bytes(const fa_paged_cache* c, int keep, size_t* pages, size_t* hol
   *holes = *pages + align256(bh * ((keep + c->page_size - 1) / c->page_size + 1) * sizeof(int));
   *movers = *holes + align256(bh * keep * sizeof(int));
   *scales = *movers + align256(bh * keep * sizeof(int));
-  return *scales + align256(bh * keep * 2 * sizeof(float));
+  return *scales + align256(bh * 2 * sizeof(float));
 }
 
 }  // namespace
@@ -229,7 +229,7 @@ fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, int* new_
   a.page_holes = reinterpret_cast<int*>(ws + p);
   a.holes = reinterpret_cast<int*>(ws + h);
   a.movers = reinterpret_cast<int*>(ws + m);
-  a.mover_scales = reinterpret_cast<float2*>(ws + s);
+  a.edge_scales = reinterpret_cast<float2*>(ws + s);
   a.status = fa::device_status_word();
   if (!a.status) return FA_ERR_CUDA;
   return fa::launch_paged_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t to_codes(float a, float b) {
   return c;
 }
 
-// to_codes for finite numbers within the type's range.
+// to_codes for numbers within the type's range, and NaN.
 template <bool E5M2>
 __device__ __forceinline__ uint32_t to_codes_finite(float a, float b) {
   uint16_t r;
@@ -54,11 +54,13 @@ __device__ __forceinline__ uint32_t to_codes_finite(float a, float b) {
   return r;
 }
 
-// Four codes times `ratio`, rounded again.
+// Four codes times `ratio` (at most 1), rounded again.
 template <bool E5M2>
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
   const float2 a = from_codes<E5M2>(c & 0xffffu), b = from_codes<E5M2>(c >> 16);
-  return to_codes<E5M2>(a.x * ratio, a.y * ratio) | (to_codes<E5M2>(b.x * ratio, b.y * ratio) << 16);
+  if (E5M2 && __vcmpeq4(c & 0x7f7f7f7fu, 0x7c7c7c7cu))  // an infinity
+    return to_codes<E5M2>(a.x * ratio, a.y * ratio) | (to_codes<E5M2>(b.x * ratio, b.y * ratio) << 16);
+  return to_codes_finite<E5M2>(a.x * ratio, a.y * ratio) | (to_codes_finite<E5M2>(b.x * ratio, b.y * ratio) << 16);
 }
 template <bool E5M2>
 __device__ __forceinline__ uint4 rescale16(uint4 c, float ratio) {
@@ -229,8 +231,8 @@ cudaError_t launch_append_t(const PagedAppendArgs& a, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- evict
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectKeys = 16;  // sort keys a thread holds in registers
+
+constexpr int kSelectKeys = 20;  // sort keys a thread holds in registers
 
 // Order of the slots as unsigned numbers: protected ones first, then NaN,
 // then the weights from large to small (-0 counts as 0).
@@ -256,41 +258,53 @@ __device__ __forceinline__ void store_remote(const void* mine, uint32_t rank, in
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
 }
 
-// Sums of three numbers over the threads of the C CTAs of a cluster, known to
-// every thread; `below` gets those of the CTAs before this one and of the threads
-// before this one (PREFIX), in thread order.
 struct Three {
   int a, b, c;
 };
-template <int C>
+// Sums over the threads of the C CTAs of a cluster (TH threads each), for every thread.
+template <int C, int TH>
 struct Gather {
-  int (*s_warp)[32][3];  // [2] turns
-  int (*s_cta)[8][3];    // [2] turns
+  unsigned (*s_sum)[3];       // [kTurns] zeros
+  int (*s_warp)[2];           // [32]
+  int (*s_cta)[8][3];         // [2] turns
   int turn = 0;
-  __device__ __forceinline__ Three sum(Three v) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    v.a = __reduce_add_sync(0xffffffffu, v.a);
-    v.b = __reduce_add_sync(0xffffffffu, v.b);
-    v.c = __reduce_add_sync(0xffffffffu, v.c);
-    int(*w)[3] = s_warp[turn];
-    if (lane == 0) w[warp][0] = v.a, w[warp][1] = v.b, w[warp][2] = v.c;
+  static constexpr int kTurns = 24;
+  // Numbers of at most 20 a thread are added up three in a word, in one
+  // reduction of the warp; larger ones (runs too long for registers) one by one.
+  __device__ __forceinline__ Three sum(Three v, bool small) {
+    const int lane = threadIdx.x & 31;
+    unsigned* at = s_sum[turn];
+    if (small) {
+      const unsigned x = __reduce_add_sync(0xffffffffu, (unsigned)v.a | (unsigned)v.b << 10 | (unsigned)v.c << 20);
+      if (lane == 0) atomicAdd(at, (x & 1023u) | (x >> 10 & 1023u) << 16);  // at most 20 * 1024 each
+      if (lane == 1) atomicAdd(at + 2, x >> 20);
+    } else {
+      v.a = __reduce_add_sync(0xffffffffu, v.a);
+      v.b = __reduce_add_sync(0xffffffffu, v.b);
+      v.c = __reduce_add_sync(0xffffffffu, v.c);
+      if (lane < 3) atomicAdd(at + lane, (unsigned)(lane == 0 ? v.a : lane == 1 ? v.b : v.c));
+    }
     __syncthreads();
-    v.a = __reduce_add_sync(0xffffffffu, w[lane][0]);
-    v.b = __reduce_add_sync(0xffffffffu, w[lane][1]);
-    v.c = __reduce_add_sync(0xffffffffu, w[lane][2]);
+    v.a = (int)(small ? at[0] & 0xffffu : at[0]);
+    v.b = (int)(small ? at[0] >> 16 : at[1]);
+    v.c = (int)at[2];
     if (C > 1) {
-      int* mine = s_cta[turn][cluster_rank()];
-      if (threadIdx.x < 3 * C) store_remote(mine + threadIdx.x % 3, threadIdx.x / 3, threadIdx.x % 3 == 0 ? v.a : threadIdx.x % 3 == 1 ? v.b : v.c);
+      int(*all)[3] = s_cta[turn & 1];
+      int* mine = all[cluster_rank()];
+      if (threadIdx.x < 3 * C) {
+        const int i = threadIdx.x % 3;
+        store_remote(mine + i, threadIdx.x / 3, i == 0 ? v.a : i == 1 ? v.b : v.c);
+      }
       cluster_sync();
       v.a = v.b = v.c = 0;
 #pragma unroll
       for (int r = 0; r < C; ++r) {
-        v.a += s_cta[turn][r][0];
-        v.b += s_cta[turn][r][1];
-        v.c += s_cta[turn][r][2];
+        v.a += all[r][0];
+        v.b += all[r][1];
+        v.c += all[r][2];
       }
     }
-    turn ^= 1;
+    ++turn;
     return v;
   }
   // Exclusive prefix sums of a and b over all threads of the cluster, in order.
@@ -302,10 +316,10 @@ struct Gather {
       const int p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) x += p, y += q;
     }
-    int(*w)[3] = s_warp[turn];
-    if (lane == 31) w[warp][0] = x, w[warp][1] = y;
+    __syncthreads();  // the list may still be read from the call before
+    if (lane == 31) s_warp[warp][0] = x, s_warp[warp][1] = y;
     __syncthreads();
-    const int wa = w[lane][0], wb = w[lane][1];
+    const int wa = lane < TH / 32 ? s_warp[lane][0] : 0, wb = lane < TH / 32 ? s_warp[lane][1] : 0;
     Three r, all;
     r.a = x - v.a + __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);
     r.b = y - v.b + __reduce_add_sync(0xffffffffu, lane < warp ? wb : 0);
@@ -314,18 +328,18 @@ struct Gather {
     r.c = all.c = 0;
     if (C > 1) {
       const int rank = (int)cluster_rank();
-      int* mine = s_cta[turn][rank];
-      if (threadIdx.x < 2 * C) store_remote(mine + (threadIdx.x & 1), threadIdx.x >> 1, threadIdx.x & 1 ? all.b : all.a);
+      int(*of)[3] = s_cta[turn & 1];
+      if (threadIdx.x < 2 * C) store_remote(of[rank] + (threadIdx.x & 1), threadIdx.x >> 1, threadIdx.x & 1 ? all.b : all.a);
       cluster_sync();
       all.a = all.b = 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (c < rank) r.a += s_cta[turn][c][0], r.b += s_cta[turn][c][1];
-        all.a += s_cta[turn][c][0];
-        all.b += s_cta[turn][c][1];
+        if (c < rank) r.a += of[c][0], r.b += of[c][1];
+        all.a += of[c][0];
+        all.b += of[c][1];
       }
     }
-    turn ^= 1;
+    ++turn;
     *total = all;
     return r;
   }
@@ -333,17 +347,20 @@ struct Gather {
 
 // One cluster of C CTAs a (sequence, head): which slots leave, and which of the
 // kept ones move where.  A thread owns a run of consecutive slots, its keys
-// in registers (up to 16; longer runs are read again in every pass).  The
+// in registers (up to 20; longer runs are read again in every pass).  The
 // m-th largest key is found two bits at a time (three counts a step over all
 // keys), at most 16 steps whatever the distribution, fewer where a count
 // meets m earlier, and no atomics on data.  Equal keys: the lowest slots stay.
 // Prefix sums over the runs then give every hole and every mover its place in
 // slot order.  Reads 8 bytes a slot; the steps are bound by their barriers
-// (2080 slots: 27 us with keys in shared memory, 1024 strided, and counts by
-// atomics).
-template <int C>
-__global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __grid_constant__ PagedEvictArgs a) {
-  __shared__ int s_warp[2][32][3];
+// and by the reductions, so small CTAs and one reduction a step (2080 slots
+// for 32 x 8 heads: 27 us with 1024 threads and three reductions).
+template <int C, int TH>
+__global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant__ PagedEvictArgs a) {
+  constexpr int K = kSelectKeys;
+  using Sums = Gather<C, TH>;
+  __shared__ unsigned s_sum[Sums::kTurns][3];
+  __shared__ int s_warp[32][2];
   __shared__ int s_cta[2][8][3];
   const int bh = blockIdx.x / C, b = bh / a.c.Hkv, h = bh % a.c.Hkv;
   const int rank = C > 1 ? (int)cluster_rank() : 0;
@@ -367,45 +384,44 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
   const float* weight = a.weight_acc + state;
   const int* position = a.positions + state;
   // runs of a multiple of four slots
-  const int run = ((n + kSelectThreads * C - 1) / (kSelectThreads * C) + 3) & ~3;
-  const long long begin = (long long)(rank * kSelectThreads + tid) * run;
+  const int run = ((n + TH * C - 1) / (TH * C) + 3) & ~3;
+  const long long begin = (long long)(rank * TH + tid) * run;
   const int s0 = (int)(begin < n ? begin : n), s1 = min(n, s0 + run);
-  const bool cached = run <= kSelectKeys;
-  Gather<C> gather = {s_warp, s_cta};
+  const bool cached = run <= K;
+  Sums gather = {s_sum, s_warp, s_cta};
+  if (tid < 3 * Sums::kTurns) s_sum[tid / 3][tid % 3] = 0;
+  if (C > 1) cluster_sync();  // all CTAs of the cluster are there
+  else __syncthreads();
 
   int latest = INT_MIN, bad = 0;
-  float w[kSelectKeys];
-  int p[kSelectKeys];
-  if (cached) {
+  // four slots' weights and positions (0 and the lowest number where there is none)
+  auto load4 = [&](int s, float (&w)[4], int (&p)[4]) {
+    if (s + 4 <= s1) {
+      const float4 x = *reinterpret_cast<const float4*>(weight + s);
+      const int4 y = *reinterpret_cast<const int4*>(position + s);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+      p[0] = y.x, p[1] = y.y, p[2] = y.z, p[3] = y.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < kSelectKeys; i += 4) {
-      if (i < run && s0 + i + 4 <= s1) {
-        const float4 x = *reinterpret_cast<const float4*>(weight + s0 + i);
-        const int4 y = *reinterpret_cast<const int4*>(position + s0 + i);
-        w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
-        p[i] = y.x, p[i + 1] = y.y, p[i + 2] = y.z, p[i + 3] = y.w;
-      } else {
-#pragma unroll
-        for (int k = i; k < i + 4; ++k) {
-          const bool in = k < run && s0 + k < s1;
-          w[k] = in ? weight[s0 + k] : 0.f;
-          p[k] = in ? position[s0 + k] : INT_MIN;
-        }
+      for (int k = 0; k < 4; ++k) {
+        w[k] = s + k < s1 ? weight[s + k] : 0.f;
+        p[k] = s + k < s1 ? position[s + k] : INT_MIN;
       }
     }
-#pragma unroll
-    for (int i = 0; i < kSelectKeys; ++i) latest = max(latest, p[i]);
-  } else {
-    for (int s = s0; s < s1; ++s) latest = max(latest, position[s]);
+  };
+  for (int s = s0; s < s1; s += 4) {
+    float w[4];
+    int p[4];
+    load4(s, w, p);
+    latest = max(max(latest, max(p[0], p[1])), max(p[2], p[3]));
   }
-  for (int t = rank * kSelectThreads + tid; t < (n + ps - 1) / ps; t += kSelectThreads * C)
+  for (int t = rank * TH + tid; t < (n + ps - 1) / ps; t += TH * C)
     bad |= table[t] < 0 || table[t] >= a.c.pages;
-  {  // the largest position, in two halves of 16 bits that add up; and bad pages
+  {  // the largest position
     latest = __reduce_max_sync(0xffffffffu, latest);
-    int(*x)[3] = s_warp[1];
-    if ((tid & 31) == 0) x[tid >> 5][0] = latest;
+    if ((tid & 31) == 0) s_warp[tid >> 5][0] = latest;
     __syncthreads();
-    latest = __reduce_max_sync(0xffffffffu, x[tid & 31][0]);
+    latest = __reduce_max_sync(0xffffffffu, s_warp[tid & (TH / 32 - 1)][0]);
     if (C > 1) {
       if (tid < C) store_remote(s_cta[1][rank], tid, latest);
       cluster_sync();
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
       for (int r = 0; r < C; ++r) latest = max(latest, s_cta[1][r][0]);
     }
   }
-  if (gather.sum({bad, 0, 0}).a) {  // reported; the sequence stays as it is (every head sees the same row)
+  if (gather.sum({bad, 0, 0}, true).a) {  // reported; the sequence stays as it is (every head sees the same row)
     if (speaks) {
       if (h == 0) {
         atomicOr(a.status, kStatusBadPages);
@@ -423,10 +439,19 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     }
     return;
   }
-  uint32_t key[kSelectKeys];
+  uint32_t key[K];
 #pragma unroll
-  for (int i = 0; i < kSelectKeys; ++i)
-    key[i] = cached && i < run && s0 + i < s1 ? rank_key(w[i], p[i], latest, a.recent) : 0u;
+  for (int i = 0; i < K; i += 4) {
+    key[i] = key[i + 1] = key[i + 2] = key[i + 3] = 0u;
+    if (cached && i < run) {
+      float w[4];
+      int p[4];
+      load4(s0 + i, w, p);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (s0 + i + k < s1) key[i + k] = rank_key(w[k], p[k], latest, a.recent);
+    }
+  }
   auto key_at = [&](int s) { return rank_key(weight[s], position[s], latest, a.recent); };
 
   // The largest v with at least m keys >= v (keys of slots are at least 0x007fffff, 0 is none).
@@ -438,7 +463,8 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     Three c = {0, 0, 0};
     if (cached) {
 #pragma unroll
-      for (int i = 0; i < kSelectKeys; ++i) {
+      for (int i = 0; i < K; ++i) {
+        if (i >= run) break;  // the same for all threads
         c.a += key[i] >= t1;
         c.b += key[i] >= t2;
         c.c += key[i] >= t3;
@@ -451,7 +477,7 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
         c.c += k >= t3;
       }
     }
-    c = gather.sum(c);
+    c = gather.sum(c, cached);
     if (c.c >= m) v = t3, at_least = c.c;
     else if (c.b >= m) v = t2, at_least = c.b;
     else if (c.a >= m) v = t1, at_least = c.a;
@@ -462,7 +488,7 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     Three mine = {0, 0, 0}, all;
     if (cached) {
 #pragma unroll
-      for (int i = 0; i < kSelectKeys; ++i) mine.a += key[i] > v, mine.b += key[i] == v;
+      for (int i = 0; i < K; ++i) mine.a += key[i] > v, mine.b += key[i] == v;
     } else {
       for (int s = s0; s < s1; ++s) {
         const uint32_t k = key_at(s);
@@ -482,7 +508,7 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     int e = eq;
     if (cached) {
 #pragma unroll
-      for (int i = 0; i < kSelectKeys; ++i)
+      for (int i = 0; i < K; ++i)
         if (i < run && s0 + i < s1) {
           const bool yes = kept(key[i], e);
           mine.a += !yes && s0 + i < m;
@@ -509,7 +535,7 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
   };
   if (cached) {
 #pragma unroll
-    for (int i = 0; i < kSelectKeys; ++i)
+    for (int i = 0; i < K; ++i)
       if (i < run && s0 + i < s1) put(s0 + i, key[i]);
   } else {
     for (int s = s0; s < s1; ++s) put(s, key_at(s));
@@ -518,112 +544,121 @@ __global__ void __launch_bounds__(kSelectThreads) paged_select_kernel(const __gr
     page_holes[pages] = all.a;
     a.plan_count[bh] = all.a;
     if (h == 0) a.new_lens[b] = m;
-  }
-  // The scales of the movers' pages: the moving kernel may change that of the page where the kept part ends.
-  if (C > 1) cluster_sync();
-  else __syncthreads();
-  for (int i = rank * kSelectThreads + tid; i < all.b; i += kSelectThreads * C) {
-    const long long at = (long long)table[__ldcg(a.movers + list + i) / ps] * a.c.Hkv + h;
-    a.mover_scales[list + i] = make_float2(a.c.k_scale[at], a.c.v_scale[at]);
+    if (m & (ps - 1)) {  // the moving kernel may change the scales of the page where the kept part ends
+      const long long at = (long long)table[pages - 1] * a.c.Hkv + h;
+      a.edge_scales[bh] = make_float2(a.c.k_scale[at], a.c.v_scale[at]);
+    }
   }
   if (C > 1) cluster_sync();  // no CTA leaves while another may still write to its shared memory
 }
 
-// One CTA a (page before the new length, sequence and head): the movers that
+// One warp a (page before the new length, sequence and head): the movers that
 // go into the page's holes, the page's slots that stay, at one scale.  A
 // mover's own page may be the page where the kept part ends and be rewritten
-// at the same time by its own CTA: its rows behind the new length are not
-// touched there, and its scale was noted by the kernel before.
+// at the same time by its own warp: its rows behind the new length are not
+// touched there, and its scales were noted by the kernel before.  The chain of
+// dependent reads (list, table, codes) is what it waits for, so pages go to
+// warps, not CTAs, and each keeps several rows under way.
+constexpr int kMoveWarps = 8;
 template <bool E5M2>
-__global__ void __launch_bounds__(256) paged_move_kernel(const __grid_constant__ PagedEvictArgs a) {
-  __shared__ uint32_t s_hole[4];
-  __shared__ int s_to[128], s_from[128];  // a mover's row in the page, and its row in the pool (page * ps + row)
-  __shared__ long long s_src[128];
-  __shared__ float s_k[128], s_v[128];
-  __shared__ float s_top[2][4];
+__global__ void __launch_bounds__(32 * kMoveWarps, 5) paged_move_kernel(const __grid_constant__ PagedEvictArgs a) {
+  struct List {
+    long long src[128];  // a mover's row in the pool, in elements
+    float k[128], v[128];
+    int to[128];  // its row in the page
+    uint32_t hole[4];
+  };
+  __shared__ List lists[kMoveWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y, b = bh / a.c.Hkv, h = bh % a.c.Hkv;
-  const int ps = a.c.ps, d = a.c.d, tid = threadIdx.x;
+  const int ps = a.c.ps, d = a.c.d;
   const int m = a.keep;  // a sequence that loses slots keeps exactly `keep`
-  const int start = blockIdx.x * ps, end = min(m, start + ps);
-  const int pages = (m + ps - 1) / ps;
-  if (tid < 4) s_hole[tid] = 0;
+  const int pages = (m + ps - 1) / ps, t = blockIdx.x * kMoveWarps + warp;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (t >= pages) return;
+  List& x = lists[warp];
   const int* table = a.c.table + (long long)b * a.c.width;
-  const int2 at_page = make_int2(a.page_holes[(long long)bh * (pages + 1) + blockIdx.x],
-                                 a.page_holes[(long long)bh * (pages + 1) + blockIdx.x + 1]);
-  const int page = table[blockIdx.x];
-  const int count = a.plan_count[bh];
-  if (count == 0) return;  // nothing leaves, or the sequence was reported: the lists are not set
-  const int lo = at_page.x, cnt = at_page.y - lo;
-  if (cnt == 0) return;
+  const int* page_holes = a.page_holes + (long long)bh * (pages + 1) + t;
+  const int lo = page_holes[0], cnt = page_holes[1] - lo;
+  const int page = table[t];
+  // nothing leaves, or the sequence was reported (the lists are not set then); no hole in this page
+  if (a.plan_count[bh] == 0 || cnt == 0) return;
+  const int start = t * ps, rows = min(m, start + ps) - start;
   const long long list = (long long)bh * m + lo;
   const long long state = (long long)bh * a.c.width * ps;
   const long long own_scale = (long long)page * a.c.Hkv + h;
-  const bool stays = end - start > cnt;  // slots of the page that stay
+  const bool stays = rows > cnt;  // slots of the page that stay
   const float k_was = a.c.k_scale[own_scale], v_was = a.c.v_scale[own_scale];
-  __syncthreads();
-  float k_now = 0.f, v_now = 0.f;
-  if (tid < 128) {  // a page has at most 128 slots
-    if (tid < cnt) {
-      const int to = a.holes[list + tid], from = a.movers[list + tid];
-      const float2 s = a.mover_scales[list + tid];
-      s_to[tid] = to - start;
-      s_src[tid] = (((long long)table[from / ps] * a.c.Hkv + h) * ps + from % ps) * d;
-      s_k[tid] = k_now = s.x;
-      s_v[tid] = v_now = s.y;
-      atomicOr(&s_hole[(to - start) >> 5], 1u << ((to - start) & 31));
-      a.weight_acc[state + to] = a.weight_acc[state + from];
-      a.positions[state + to] = a.positions[state + from];
-    }
+  if (lane < 4) x.hole[lane] = 0;
+  __syncwarp();
+  float k_now = stays ? k_was : 0.f, v_now = stays ? v_was : 0.f;
+  for (int i = lane; i < cnt; i += 32) {
+    const int to = a.holes[list + i], from = a.movers[list + i];
+    const long long at = (long long)table[from >> a.c.ps_shift] * a.c.Hkv + h;
+    const float2 s = from >> a.c.ps_shift == pages - 1 ? a.edge_scales[bh] : make_float2(a.c.k_scale[at], a.c.v_scale[at]);
+    x.to[i] = to - start;
+    x.src[i] = (at * ps + (from & (ps - 1))) * d;
+    x.k[i] = s.x;
+    x.v[i] = s.y;
+    k_now = fmaxf(k_now, s.x);
+    v_now = fmaxf(v_now, s.y);
+    atomicOr(&x.hole[(to - start) >> 5], 1u << ((to - start) & 31));
+    a.weight_acc[state + to] = a.weight_acc[state + from];
+    a.positions[state + to] = a.positions[state + from];
+  }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      k_now = fmaxf(k_now, __shfl_xor_sync(0xffffffffu, k_now, o));
-      v_now = fmaxf(v_now, __shfl_xor_sync(0xffffffffu, v_now, o));
-    }
-    if ((tid & 31) == 0) s_top[0][tid >> 5] = k_now, s_top[1][tid >> 5] = v_now;
+  for (int o = 16; o > 0; o >>= 1) {
+    k_now = fmaxf(k_now, __shfl_xor_sync(0xffffffffu, k_now, o));
+    v_now = fmaxf(v_now, __shfl_xor_sync(0xffffffffu, v_now, o));
   }
-  __syncthreads();
-  k_now = fmaxf(fmaxf(s_top[0][0], s_top[0][1]), fmaxf(s_top[0][2], s_top[0][3]));
-  v_now = fmaxf(fmaxf(s_top[1][0], s_top[1][1]), fmaxf(s_top[1][2], s_top[1][3]));
-  if (stays) {
-    k_now = fmaxf(k_now, k_was);
-    v_now = fmaxf(v_now, v_was);
-  }
+  __syncwarp();
   const int lanes = d / 16;  // 16 codes a thread: 4, 8 or 16 threads a row
-  const int lane = tid % lanes, group = tid / lanes, groups = 256 / lanes;
+  const int sub = lane % lanes, group = lane / lanes, groups = 32 / lanes;
   const long long own = own_scale * ps * d;
+  uint4* own_k = reinterpret_cast<uint4*>(a.c.k_pages + own) + sub;
+  uint4* own_v = reinterpret_cast<uint4*>(a.c.v_pages + own) + sub;
   if (stays && (k_now != k_was || v_now != v_was)) {
     const float kr = k_was / k_now, vr = v_was / v_now;
-    for (int s = group; s < end - start; s += groups) {
-      if (s_hole[s >> 5] >> (s & 31) & 1u) continue;
-      uint4* kp = reinterpret_cast<uint4*>(a.c.k_pages + own + (long long)s * d) + lane;
-      uint4* vp = reinterpret_cast<uint4*>(a.c.v_pages + own + (long long)s * d) + lane;
-      uint4 kc = *kp, vc = *vp;
-      if (k_now != k_was) *kp = rescale16<E5M2>(kc, kr);
-      if (v_now != v_was) *vp = rescale16<E5M2>(vc, vr);
+#pragma unroll 2
+    for (int r = group; r < rows; r += groups) {
+      if (x.hole[r >> 5] >> (r & 31) & 1u) continue;
+      if (k_now != k_was) own_k[r * lanes] = rescale16<E5M2>(own_k[r * lanes], kr);
+      if (v_now != v_was) own_v[r * lanes] = rescale16<E5M2>(own_v[r * lanes], vr);
     }
   }
-#pragma unroll 2
-  for (int i = group; i < cnt; i += groups) {
-    const long long src = s_src[i], dst = own + (long long)s_to[i] * d;
-    uint4 kc = reinterpret_cast<const uint4*>(a.c.k_pages + src)[lane];
-    uint4 vc = reinterpret_cast<const uint4*>(a.c.v_pages + src)[lane];
-    if (s_k[i] != k_now) kc = rescale16<E5M2>(kc, s_k[i] / k_now);
-    if (s_v[i] != v_now) vc = rescale16<E5M2>(vc, s_v[i] / v_now);
-    reinterpret_cast<uint4*>(a.c.k_pages + dst)[lane] = kc;
-    reinterpret_cast<uint4*>(a.c.v_pages + dst)[lane] = vc;
+  constexpr int U = 2;  // rows under way (four: as fast, and half as many warps fit on an SM)
+  for (int i0 = group; i0 < cnt; i0 += U * groups) {
+    uint4 kc[U], vc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * groups;
+      if (i < cnt) {
+        kc[u] = reinterpret_cast<const uint4*>(a.c.k_pages + x.src[i])[sub];
+        vc[u] = reinterpret_cast<const uint4*>(a.c.v_pages + x.src[i])[sub];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * groups;
+      if (i < cnt) {
+        if (x.k[i] != k_now) kc[u] = rescale16<E5M2>(kc[u], x.k[i] / k_now);
+        if (x.v[i] != v_now) vc[u] = rescale16<E5M2>(vc[u], x.v[i] / v_now);
+        own_k[x.to[i] * lanes] = kc[u];
+        own_v[x.to[i] * lanes] = vc[u];
+      }
+    }
   }
-  if (tid == 0) {
+  if (lane == 0) {
     if (k_now != k_was) a.c.k_scale[own_scale] = k_now;
     if (v_now != v_was) a.c.v_scale[own_scale] = v_now;
   }
 }
 
-template <int C>
+template <int C, int TH>
 cudaError_t launch_select(const PagedEvictArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.c.B * a.c.Hkv * C));
-  cfg.blockDim = dim3(kSelectThreads);
+  cfg.blockDim = dim3(TH);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -631,7 +666,7 @@ cudaError_t launch_select(const PagedEvictArgs& a, cudaStream_t stream) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_select_kernel<C>, a);
+  return cudaLaunchKernelEx(&cfg, paged_select_kernel<C, TH>, a);
 }
 
 }  // namespace
@@ -641,23 +676,25 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream) {
-  // CTAs a head: as many as hold its slots' keys in registers, more while
-  // SMs are idle and each still has 4096 slots.
+  // One CTA of 256 threads a head where its slots' keys fit in its registers
+  // (5120), else 1024 threads, else a cluster of those: a step of the search
+  // costs 0.5 us in a CTA and 1.25 us in a cluster (its barriers), which was
+  // more than eight CTAs of 256 threads gained on a head of 16384 slots.
   const int BH = a.c.B * a.c.Hkv;
   const long long slots = (long long)a.c.width * a.c.ps;
-  const int sms = sm_count();
+  const bool small = slots <= 256 * kSelectKeys;
   int c = 1;
-  while (c < 8 && ((long long)c * kSelectThreads * kSelectKeys < slots ||
-                   (2LL * c * BH <= sms && slots / (2 * c) >= 4096)))
-    c *= 2;
-  cudaError_t e = c == 1   ? launch_select<1>(a, stream)
-                  : c == 2 ? launch_select<2>(a, stream)
-                  : c == 4 ? launch_select<4>(a, stream)
-                           : launch_select<8>(a, stream);
+  while (c < 8 && (long long)1024 * kSelectKeys * c < slots) c *= 2;
+  cudaError_t e = small    ? launch_select<1, 256>(a, stream)
+                  : c == 1 ? launch_select<1, 1024>(a, stream)
+                  : c == 2 ? launch_select<2, 1024>(a, stream)
+                  : c == 4 ? launch_select<4, 1024>(a, stream)
+                           : launch_select<8, 1024>(a, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.keep + a.c.ps - 1) / a.c.ps), (unsigned)BH);
-  cfg.blockDim = dim3(256);
+  const int pages = (a.keep + a.c.ps - 1) / a.c.ps;
+  cfg.gridDim = dim3((unsigned)((pages + kMoveWarps - 1) / kMoveWarps), (unsigned)BH);
+  cfg.blockDim = dim3(32 * kMoveWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -123,7 +123,7 @@ def test_workspace_sizes(lib):
     # slots that cannot be merged
     assert size(cache(pages_per_seq=1 << 20, num_pages=1 << 21), 8, 1, 0, 0, 0) == 0
     ev = lib.fa_paged_evict_workspace_size
-    assert ev(cache(), 100) == 256 + 256 + 2 * 3328 + 6400 and ev(cache(), 0) == 0 and ev(cache(), 513) == 0
+    assert ev(cache(), 100) == 256 + 256 + 2 * 3328 + 256 and ev(cache(), 0) == 0 and ev(cache(), 513) == 0
 
 
 def test_status_has_a_name(lib):
