@@ -52,6 +52,7 @@
 #include <cuda_fp16.h>
 
 #include "fa_paged.h"
+#include "fa_pdl.cuh"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -86,9 +87,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   while (!mbar_try_wait(a, parity))
     if (global_timer_ns() - t0 > kWaitTimeoutNs) return;
 }
-
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // D(tmem) (+)= A(smem) * B(smem), one K = 32 step of 8-bit floats, fp32 accumulation.
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -240,7 +238,7 @@ struct PagedCfg {
 // the line is cut into equal pieces, and a CTA gets the tiles whose places lie
 // in its piece.  (The start and end of a head's segment take about as long as
 // kHeadCost tiles.)
-constexpr int kHeadCost = 2;
+constexpr int kHeadCost = 4;
 struct Share {
   long long total;  // places
   int ctas;         // CTAs that get some
@@ -348,6 +346,7 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
     n = (int)(last < tb ? last : tb) - t;
   };
   if (warp == 4 * G + 2) {
+    pdl_wait();
     if (a.balanced) {
       int mine = 0;  // tiles of sequence `lane` of the last 32 looked at
       long long total = 0;
@@ -407,6 +406,7 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();  // over by now: the walker waited
   const uint32_t tmem = *tmem_slot;
   auto read_segment = [&](int k) {
     const int4 x = *reinterpret_cast<const int4*>(smem + C::OFF_DESC + 32 * (k % C::SEGS));
@@ -1009,6 +1009,7 @@ __global__ void __launch_bounds__(256, 5) paged_finish_kernel(const __grid_const
   __shared__ float s_o[8][D];
   __shared__ float2 s_ml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch();
   if ((int)blockIdx.x < row_blocks) {
     const int row = blockIdx.x * (8 / team) + warp / team, member = warp % team;
     const bool there = row < a.c.B * a.c.Hkv * a.rows;
@@ -1133,20 +1134,6 @@ __global__ void __launch_bounds__(256, 5) paged_finish_kernel(const __grid_const
   }
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
-}
-
 template <int D, int T, int G>
 cudaError_t launch_attention_t(const PagedAttnArgs& a, cudaStream_t stream) {
   using C = PagedCfg<D, T, G>;
@@ -1157,8 +1144,7 @@ cudaError_t launch_attention_t(const PagedAttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((unsigned)a.ctas, (unsigned)((a.rows + C::R - 1) / C::R));
-  kern<<<grid, C::WARPS * 32, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kern, grid, dim3(C::WARPS * 32), smem, stream, a);
 }
 
 template <int D, int T>
@@ -1195,7 +1181,7 @@ cudaError_t launch_d(const PagedAttnArgs& a, cudaStream_t stream) {
               : width == 2 ? paged_finish_kernel<D, 2>
               : width == 4 ? paged_finish_kernel<D, 4>
                            : paged_finish_kernel<D, 8>;
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), stream, a, (int)row_blocks, team);
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, stream, a, (int)row_blocks, team);
 }
 
 }  // namespace
@@ -1211,7 +1197,7 @@ PagedPlan paged_plan(int B, int Hkv, int rows, int d, int ps, int max_len, int n
   const int tiles = (max_len + 127) / 128;
   const long long all = BH * places_of(tiles);
   constexpr int kMostTiles = kPagedMaxChunk / 128;
-  p.min_tiles = 4;
+  p.min_tiles = 6;
   int segment;  // tiles of the longest segment
   if (num_splits == 0 && tiles > 4 && B <= kPagedMaxBalanced) {
     // The device shares out what there is.  A CTA never gets more than

@@ -15,6 +15,7 @@
 #include <limits.h>
 
 #include "fa_paged.h"
+#include "fa_pdl.cuh"
 
 namespace fa {
 namespace {
@@ -95,6 +96,8 @@ __device__ __forceinline__ float scale_for(float amax) {
 // One token a sequence is bound by the launch and three dependent reads.
 template <bool E5M2, int NV>
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+  pdl_launch();
+  pdl_wait();
   const int b = blockIdx.z, h = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
   const int ps = a.c.ps, d = a.c.d;
@@ -221,13 +224,12 @@ cudaError_t launch_append_t(const PagedAppendArgs& a, cudaStream_t stream) {
   const int reach = (int)((a.N + a.c.ps - 2LL) / a.c.ps + 1);
   const dim3 grid((unsigned)reach, (unsigned)(2 * a.c.Hkv), (unsigned)a.c.B);
   switch (vecs / threads) {
-    case 1: paged_append_kernel<E5M2, 1><<<grid, threads, 0, stream>>>(a); break;
-    case 2: paged_append_kernel<E5M2, 2><<<grid, threads, 0, stream>>>(a); break;
-    case 4: paged_append_kernel<E5M2, 4><<<grid, threads, 0, stream>>>(a); break;
-    case 8: paged_append_kernel<E5M2, 8><<<grid, threads, 0, stream>>>(a); break;
+    case 1: return launch_pdl(paged_append_kernel<E5M2, 1>, grid, dim3(threads), 0, stream, a);
+    case 2: return launch_pdl(paged_append_kernel<E5M2, 2>, grid, dim3(threads), 0, stream, a);
+    case 4: return launch_pdl(paged_append_kernel<E5M2, 4>, grid, dim3(threads), 0, stream, a);
+    case 8: return launch_pdl(paged_append_kernel<E5M2, 8>, grid, dim3(threads), 0, stream, a);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- evict
@@ -366,7 +368,8 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
   const int rank = C > 1 ? (int)cluster_rank() : 0;
   const int tid = threadIdx.x, ps = a.c.ps;
   const bool speaks = rank == 0 && tid == 0;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_launch();
+  pdl_wait();
   const int n = a.lens[b];
   if (n < 0 || n > a.c.width * ps || n <= a.keep) {  // the same for the whole cluster
     if (speaks) {
@@ -574,7 +577,8 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 5) paged_move_kernel(const __
   const int ps = a.c.ps, d = a.c.d;
   const int m = a.keep;  // a sequence that loses slots keeps exactly `keep`
   const int pages = (m + ps - 1) / ps, t = blockIdx.x * kMoveWarps + warp;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_launch();
+  pdl_wait();
   if (t >= pages) return;
   List& x = lists[warp];
   const int* table = a.c.table + (long long)b * a.c.width;
@@ -660,12 +664,14 @@ cudaError_t launch_select(const PagedEvictArgs& a, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)(a.c.B * a.c.Hkv * C));
   cfg.blockDim = dim3(TH);
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = C;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = C > 1 ? 1 : 0;
+  cfg.numAttrs = C > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, paged_select_kernel<C, TH>, a);
 }
 
@@ -691,18 +697,10 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream) {
                   : c == 4 ? launch_select<4, 1024>(a, stream)
                            : launch_select<8, 1024>(a, stream);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
   const int pages = (a.keep + a.c.ps - 1) / a.c.ps;
-  cfg.gridDim = dim3((unsigned)((pages + kMoveWarps - 1) / kMoveWarps), (unsigned)BH);
-  cfg.blockDim = dim3(32 * kMoveWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return a.c.e5m2 ? cudaLaunchKernelEx(&cfg, paged_move_kernel<true>, a)
-                  : cudaLaunchKernelEx(&cfg, paged_move_kernel<false>, a);
+  const dim3 grid((unsigned)((pages + kMoveWarps - 1) / kMoveWarps), (unsigned)BH);
+  return a.c.e5m2 ? launch_pdl(paged_move_kernel<true>, grid, dim3(32 * kMoveWarps), 0, stream, a)
+                  : launch_pdl(paged_move_kernel<false>, grid, dim3(32 * kMoveWarps), 0, stream, a);
 }
 
 }  // namespace fa

@@ -114,12 +114,12 @@ def test_workspace_sizes(lib):
     assert size(big, 8, 1, 0, 1, 0) == parts(2 * 8 * 8, 8)
     # shared out evenly: a CTA for a head's start and two tiles at least, no more CTAs than fit (152 SMs without a GPU) ...
     mid = cache(pages_per_seq=16)
-    assert size(mid, 8, 1, 0, 0, 0) == parts(2 * 8 * (8 + 2) // 4, 8) + 256
+    assert size(mid, 8, 1, 0, 0, 0) == parts(2 * 8 * (8 + 4) // 6, 8) + 256
     assert size(big, 8, 1, 0, 0, 0) == parts(2 * 304, 8) + 256
     assert size(big, 80, 2, 0, 0, 0) == parts(2 * 152, 40) + 256
     # ... unless one would get more than 127 tiles
     huge = cache(pages_per_seq=1 << 15, num_pages=1 << 17)
-    assert size(huge, 8, 1, 0, 0, 0) == parts(2 * -(-8 * ((1 << 14) + 2) // 127), 8) + 256
+    assert size(huge, 8, 1, 0, 0, 0) == parts(2 * -(-8 * ((1 << 14) + 4) // 127), 8) + 256
     # slots that cannot be merged
     assert size(cache(pages_per_seq=1 << 20, num_pages=1 << 21), 8, 1, 0, 0, 0) == 0
     ev = lib.fa_paged_evict_workspace_size
