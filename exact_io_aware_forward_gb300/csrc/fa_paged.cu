@@ -171,17 +171,36 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
-// The T terms of a pair of values: codes in out[0 .. T-1].
+// The T terms of a pair of values: codes in out[0 .. T-1], each the rounding of
+// what the terms before leave, times 16 (exact: a code is a rounding of its
+// value).
 template <int T>
-__device__ __forceinline__ void split_terms(float a, float b, uint32_t (&out)[T]) {
+__device__ __forceinline__ void split_terms(uint64_t v, uint32_t (&out)[T]) {
 #pragma unroll
   for (int t = 0; t < T; ++t) {
+    float a, b;
+    f2_unpack(v, a, b);
     out[t] = to_e4m3x2(a, b);
-    if (t + 1 < T) {  // what is left, times 16: exact, the code is a rounding of the value
+    if (t + 1 < T) {
       const float2 c = from_e4m3x2(out[t]);
-      a = (a - c.x) * 16.f;
-      b = (b - c.y) * 16.f;
+      v = f2_fma(f2_pack(c.x, c.y), f2_pack(-16.f, -16.f), f2_mul(v, f2_pack(16.f, 16.f)));
     }
+  }
+}
+template <int T>
+__device__ __forceinline__ void split_terms(float a, float b, uint32_t (&out)[T]) {
+  split_terms<T>(f2_pack(a, b), out);
+}
+// Sum of the terms' columns: y[0] + y[1] / 16 + y[2] / 256, eight rows in pairs.
+template <int T>
+__device__ __forceinline__ void join_terms(const float (&y)[T][8], uint64_t (&out)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint64_t z = f2_pack(y[T - 1][2 * i], y[T - 1][2 * i + 1]);
+#pragma unroll
+    for (int u = T - 2; u >= 0; --u)
+      z = f2_fma(z, f2_pack(0.0625f, 0.0625f), f2_pack(y[u][2 * i], y[u][2 * i + 1]));
+    out[i] = z;
   }
 }
 
@@ -316,7 +335,7 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
     }
     for (int i = 0; i < C::SEGS; ++i) {
       mbar_init(&seg_pages[i], 1);
-      mbar_init(&seg_ready[i], 1);
+      mbar_init(&seg_ready[i], G == 1 ? 1 : 1 + 2 * G);
       mbar_init(&seg_free[i], 4 * G + 1);
     }
     mbar_init(o_free, 4 * G);
@@ -416,6 +435,81 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
     return g;
   };
 
+  // Turns rows r0 .. r1 - 1 of segment k's queries into e4m3 terms, four rows
+  // at a time, eight lanes a row, the next four on their way; `between` is run
+  // while the first are.  The row loop is kept rolled: instructions that run
+  // once cost more to fetch than to run.
+  auto fill_rows = [&](int k, const Segment& g, int r0, int r1, auto between) {
+    constexpr int E = D / 8;  // neighbouring elements of a row a lane
+    constexpr int L = E / 8;  // 16-byte loads of them
+    const int buf = k % C::SEGS, sub = lane >> 3, col = (lane & 7) * E;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((long long)g.bh * a.rows + row0) * D + col;
+    uint8_t* q8 = sQ + buf * C::Q_BYTES + (col / C::W) * (C::NB * C::W);
+    float* qinv = reinterpret_cast<float*>(smem + C::OFF_ROW) + buf * 2 * R;
+    int* row_end = reinterpret_cast<int*>(qinv + R);
+    uint4 raw[L], then[L];
+    auto load = [&](int r, uint4 (&to)[L]) {
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        to[i] = r < nr && r < r1 ? reinterpret_cast<const uint4*>(q + (long long)r * D)[i] : make_uint4(0, 0, 0, 0);
+    };
+    load(r0 + sub, raw);
+    between();
+#pragma unroll 1
+    for (int r = r0 + sub; r < r1; r += 4) {
+      load(r + 4, then);
+      float x[E];
+      uint32_t top = 0;  // the largest magnitude's bits: infinities and NaN come out on top
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const uint4& u = raw[i / 8];
+        const uint32_t two = i % 8 == 0 ? u.x : i % 8 == 2 ? u.y : i % 8 == 4 ? u.z : u.w;
+        if (a.bf16) {
+          x[i] = __uint_as_float(two << 16);
+          x[i + 1] = __uint_as_float(two & 0xffff0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+          x[i] = f.x;
+          x[i + 1] = f.y;
+        }
+        top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(x[i + 1]) & 0x7fffffffu));
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool finite = top < 0x7f800000u;
+      // 2^e with max * 2^e in [128, 256) (subnormal rows: at most 2^120)
+      const int e = finite ? min(134 - static_cast<int>(top >> 23), 120) : 0;
+      const float up = __int_as_float((e + 127) << 23);
+      uint32_t words[T][E / 4];
+#pragma unroll
+      for (int i = 0; i < E; i += 4) {
+        uint32_t lo[T], hi[T];
+        split_terms<T>(finite ? x[i] * up : 0.f, finite ? x[i + 1] * up : 0.f, lo);
+        split_terms<T>(finite ? x[i + 2] * up : 0.f, finite ? x[i + 3] * up : 0.f, hi);
+#pragma unroll
+        for (int u = 0; u < T; ++u) words[u][i / 4] = lo[u] | hi[u] << 16;
+      }
+#pragma unroll
+      for (int u = 0; u < T; ++u) {
+        if constexpr (E == 8) {
+          *reinterpret_cast<uint2*>(q8 + sw_offset<C::W>(u * R + r, col % C::W)) = make_uint2(words[u][0], words[u][1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < E / 16; ++i)
+            *reinterpret_cast<uint4*>(q8 + sw_offset<C::W>(u * R + r, col % C::W + 16 * i)) =
+                make_uint4(words[u][4 * i], words[u][4 * i + 1], words[u][4 * i + 2], words[u][4 * i + 3]);
+        }
+      }
+      if ((lane & 7) == 0) {
+        // a row that holds a NaN or an infinity has no softmax: its scores are NaN
+        qinv[r] = finite ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fc00000);
+        row_end[r] = a.causal ? g.len - a.Nq + (row0 + r) % a.Nq + 1 : g.len;
+      }
+#pragma unroll
+      for (int i = 0; i < L; ++i) raw[i] = then[i];
+    }
+  };
+
   if (warp == 4 * G + 2) {
     // ------------------------------------------------------------ segments
     // Walks this CTA's tiles segment by segment (a run of tiles of one head),
@@ -472,87 +566,24 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
       advance();
     }
   } else if (warp == 4 * G + 3) {
-    // ------------------------------------------------------------ scales and queries
-    // Turns the segment's query rows into e4m3 terms and fetches its scales:
-    // four rows at a time, eight lanes a row, the next four on their way.  The
-    // row loop is kept rolled: instructions that run once cost more to fetch
-    // than to run.
-    constexpr int E = D / 8;   // neighbouring elements of a row a lane
-    constexpr int L = E / 8;   // 16-byte loads of them
-    const int sub = lane >> 3, col = (lane & 7) * E;
+    // ------------------------------------------------------------ scales (and queries of one group)
     for (int k = 0;; ++k) {
       const int buf = k % C::SEGS;
       if (!warp_wait(&seg_pages[buf], (k / C::SEGS) & 1, abort_flag, a.status)) break;
       const Segment g = read_segment(k);
       const int head = g.bh % a.c.Hkv;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((long long)g.bh * a.rows + row0) * D + col;
-      uint8_t* q8 = sQ + buf * C::Q_BYTES + (col / C::W) * (C::NB * C::W);
-      float* qinv = reinterpret_cast<float*>(smem + C::OFF_ROW) + buf * 2 * R;
-      int* row_end = reinterpret_cast<int*>(qinv + R);
-      uint4 raw[L], then[L];
-      auto load = [&](int r, uint4 (&to)[L]) {
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-          to[i] = r < nr && g.n > 0 ? reinterpret_cast<const uint4*>(q + (long long)r * D)[i] : make_uint4(0, 0, 0, 0);
+      auto scales = [&]() {
+        for (int i = lane; i < g.pages; i += 32) {
+          const int id = s_page[buf * ne + i];
+          s_ks[buf * ne + i] = id >= 0 ? a.c.k_scale[(long long)id * a.c.Hkv + head] * a.scale_log2 : 0.f;
+          s_vs[buf * ne + i] = id >= 0 ? a.c.v_scale[(long long)id * a.c.Hkv + head] : 0.f;
+        }
       };
-      load(sub, raw);
-      for (int i = lane; g.n > 0 && i < g.pages; i += 32) {
-        const int id = s_page[buf * ne + i];
-        s_ks[buf * ne + i] = id >= 0 ? a.c.k_scale[(long long)id * a.c.Hkv + head] * a.scale_log2 : 0.f;
-        s_vs[buf * ne + i] = id >= 0 ? a.c.v_scale[(long long)id * a.c.Hkv + head] : 0.f;
-      }
-#pragma unroll 1
-      for (int r = sub; g.n > 0 && r < R; r += 4) {
-        load(r + 4, then);
-        float x[E];
-        uint32_t top = 0;  // the largest magnitude's bits: infinities and NaN come out on top
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          const uint4& u = raw[i / 8];
-          const uint32_t two = i % 8 == 0 ? u.x : i % 8 == 2 ? u.y : i % 8 == 4 ? u.z : u.w;
-          if (a.bf16) {
-            x[i] = __uint_as_float(two << 16);
-            x[i + 1] = __uint_as_float(two & 0xffff0000u);
-          } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-            x[i] = f.x;
-            x[i + 1] = f.y;
-          }
-          top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(x[i + 1]) & 0x7fffffffu));
-        }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const bool finite = top < 0x7f800000u;
-        // 2^e with max * 2^e in [128, 256) (subnormal rows: at most 2^120)
-        const int e = finite ? min(134 - static_cast<int>(top >> 23), 120) : 0;
-        const float up = __int_as_float((e + 127) << 23);
-        uint32_t words[T][E / 4];
-#pragma unroll
-        for (int i = 0; i < E; i += 4) {
-          uint32_t lo[T], hi[T];
-          split_terms<T>(finite ? x[i] * up : 0.f, finite ? x[i + 1] * up : 0.f, lo);
-          split_terms<T>(finite ? x[i + 2] * up : 0.f, finite ? x[i + 3] * up : 0.f, hi);
-#pragma unroll
-          for (int u = 0; u < T; ++u) words[u][i / 4] = lo[u] | hi[u] << 16;
-        }
-#pragma unroll
-        for (int u = 0; u < T; ++u) {
-          if constexpr (E == 8) {
-            *reinterpret_cast<uint2*>(q8 + sw_offset<C::W>(u * R + r, col % C::W)) = make_uint2(words[u][0], words[u][1]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < E / 16; ++i)
-              *reinterpret_cast<uint4*>(q8 + sw_offset<C::W>(u * R + r, col % C::W + 16 * i)) =
-                  make_uint4(words[u][4 * i], words[u][4 * i + 1], words[u][4 * i + 2], words[u][4 * i + 3]);
-          }
-        }
-        if ((lane & 7) == 0) {
-          // a row that holds a NaN or an infinity has no softmax: its scores are NaN
-          qinv[r] = finite ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fc00000);
-          row_end[r] = a.causal ? g.len - a.Nq + (row0 + r) % a.Nq + 1 : g.len;
-        }
-#pragma unroll
-        for (int i = 0; i < L; ++i) raw[i] = then[i];
+      if (g.n > 0) {
+        if (G == 1)
+          fill_rows(k, g, 0, 8, scales);
+        else
+          scales();
       }
       fence_async_smem();
       __syncwarp();
@@ -718,17 +749,35 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
     uint64_t* my_exchange = exchange + (warp >> 2) * 2;
     float* my_max = reinterpret_cast<float*>(smem + C::OFF_MAX) + (warp >> 2) * 64;
     float* my_sum = reinterpret_cast<float*>(smem + C::OFF_SUM) + (warp >> 2) * 32;
-    // byte of this slot in row r of the weights, r = 0 .. 7 of the group
-    const uint32_t p_row = smem_u32(sP) + g8 * 128 + (key & 15);
-    const int chunk16 = key >> 4;
+    // byte of this slot in row 0 of the group's weights; row r is at 128 r with
+    // the 16-byte chunk XORed with r (the buffer begins on a 1024-byte boundary)
+    const uint32_t p_byte = smem_u32(sP) + g8 * 128 + key;
+    // far below all scores, so that -inf - m is -inf
+    constexpr float kNothing = -1e30f;
     int j = 0;  // tile over all segments
     int x = 0;  // exchanges so far
     bool ok = true;
-    for (int k = 0;; ++k) {
-      if (!(ok = warp_wait(&seg_ready[k % C::SEGS], (k / C::SEGS) & 1, abort_flag, a.status))) break;
+    // With several groups two warps of each turn its rows into terms (one warp
+    // for all would take 9 us for 40 rows).  Those of the next segment before
+    // the end of this one: the MMA warp issues a tile's scores ahead of the
+    // products of the two tiles before it.
+    auto queries = [&](int k) {
+      if (G == 1) return;
+      ok = warp_wait(&seg_pages[k % C::SEGS], (k / C::SEGS) & 1, abort_flag, a.status);
+      if (ok && quarter < 2) {
+        const Segment g = read_segment(k);
+        if (g.n > 0) fill_rows(k, g, g8 + 4 * quarter, g8 + 4 * quarter + 4, []() {});
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_ready[k % C::SEGS]);
+      }
+    };
+    queries(0);
+    for (int k = 0; ok; ++k) {
+      const int buf = k % C::SEGS;
+      if (!(ok = warp_wait(&seg_ready[buf], (k / C::SEGS) & 1, abort_flag, a.status))) break;
       const Segment g = read_segment(k);
       if (g.n == 0) break;
-      const int buf = k % C::SEGS;
       const int* page = s_page + buf * ne;
       const float* qinv = reinterpret_cast<const float*>(smem + C::OFF_ROW) + buf * 2 * R + g8;
       const int* row_end = reinterpret_cast<const int*>(qinv + R);
@@ -736,12 +785,12 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
       const long long out_row = (long long)g.bh * a.rows + row0 + g8;
       const int rows_here = nr - g8;
       float* scores = a.scores + ((long long)g.bh * a.score_groups + (row0 + g8) / 8) * a.score_stride;
-      float l[8], m[8];
+      uint64_t l[4];
+      float m[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        l[r] = 0.f;
-        m[r] = neg_inf();
-      }
+      for (int r = 0; r < 8; ++r) m[r] = kNothing;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) l[r] = 0;
       for (int t = 0; t < g.n; ++t, ++j) {
         const int i = j & 1;
         const uint32_t tS = lane_base + C::COL_S + C::NB * i + g8;
@@ -752,101 +801,132 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
         const float lv = fmaxf(__log2f(fabsf(vs)), kMinLogScale), wv = vs * kWeightScale;
         if (!(ok = warp_wait(&s_full[i], (j >> 1) & 1, abort_flag, a.status))) break;
         tc_fence_after();
-        float s[8];
+        uint64_t s[4];
         {
           float y[T][8];
 #pragma unroll
           for (int u = 0; u < T; ++u) tmem_ld8(tS + u * R, y[u]);
 #pragma unroll
           for (int u = 0; u < T; ++u) tmem_ld8_wait(y[u]);
+          join_terms<T>(y, s);
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            float z = y[T - 1][r];
-#pragma unroll
-            for (int u = T - 2; u >= 0; --u) z = fmaf(z, 0.0625f, y[u][r]);
-            s[r] = z * qinv[r] * ks;
+          for (int r = 0; r < 4; r += 2) {
+            const float4 q = *reinterpret_cast<const float4*>(qinv + 2 * r);
+            s[r] = f2_mul(f2_mul(s[r], f2_pack(q.x, q.y)), f2_pack(ks, ks));
+            s[r + 1] = f2_mul(f2_mul(s[r + 1], f2_pack(q.z, q.w)), f2_pack(ks, ks));
           }
         }
         if (!live || (g.first + t) * 128 + 128 > first_end) {
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (!live || slot >= row_end[r]) s[r] = neg_inf();
+          for (int r = 0; r < 4; ++r) {
+            float y0, y1;
+            f2_unpack(s[r], y0, y1);
+            if (!live || slot >= row_end[2 * r]) y0 = neg_inf();
+            if (!live || slot >= row_end[2 * r + 1]) y1 = neg_inf();
+            s[r] = f2_pack(y0, y1);
+          }
         }
         if (a.scores != nullptr && slot < g.len && rows_here > 0) {
           float* to = scores + (long long)slot * a.score_rows;
           if (a.score_rows >= 4) {
-            *reinterpret_cast<float4*>(to) = make_float4(s[0], s[1], s[2], s[3]);
-            if (a.score_rows == 8) *reinterpret_cast<float4*>(to + 4) = make_float4(s[4], s[5], s[6], s[7]);
+            *reinterpret_cast<ulonglong2*>(to) = make_ulonglong2(s[0], s[1]);
+            if (a.score_rows == 8) *reinterpret_cast<ulonglong2*>(to + 4) = make_ulonglong2(s[2], s[3]);
           } else if (a.score_rows == 2) {
-            *reinterpret_cast<float2*>(to) = make_float2(s[0], s[1]);
+            *reinterpret_cast<uint64_t*>(to) = s[0];
           } else {
-            *to = s[0];
+            float y0, y1;
+            f2_unpack(s[0], y0, y1);
+            *to = y0;
           }
         }
         float* mine = my_max + ((x & 1) * 4 + quarter) * 8;
 #pragma unroll
-        for (int r = 0; r < 8; r += 4) {
+        for (int r = 0; r < 4; r += 2) {
           float4 top;
-          top.x = warp_max(s[r] + lv);
-          top.y = warp_max(s[r + 1] + lv);
-          top.z = warp_max(s[r + 2] + lv);
-          top.w = warp_max(s[r + 3] + lv);
-          if (lane == 0) *reinterpret_cast<float4*>(mine + r) = top;
+          f2_unpack(f2_add(s[r], f2_pack(lv, lv)), top.x, top.y);
+          f2_unpack(f2_add(s[r + 1], f2_pack(lv, lv)), top.z, top.w);
+          top.x = warp_max(top.x);
+          top.y = warp_max(top.y);
+          top.z = warp_max(top.z);
+          top.w = warp_max(top.w);
+          if (lane == 0) *reinterpret_cast<float4*>(mine + 2 * r) = top;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&my_exchange[x & 1]);
         if (!(ok = warp_wait(&my_exchange[x & 1], (x >> 1) & 1, abort_flag, a.status))) break;
         // every thread derives the same new references from the four warps' maxima
-        float corr[8];
-        bool moved = false;
+        float top[8];
         const float* all = my_max + (x & 1) * 32;
         ++x;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float top = fmaxf(fmaxf(all[r], all[8 + r]), fmaxf(all[16 + r], all[24 + r]));
-          corr[r] = 1.f;
-          if (top > m[r] + kMaxLead) {
-            corr[r] = ex2_approx(m[r] - top);
-            l[r] *= corr[r];
-            m[r] = top;
-            moved = true;
-          }
+        for (int r = 0; r < 8; r += 4) {
+          const float4 y0 = *reinterpret_cast<const float4*>(all + r);
+          const float4 y1 = *reinterpret_cast<const float4*>(all + 8 + r);
+          const float4 y2 = *reinterpret_cast<const float4*>(all + 16 + r);
+          const float4 y3 = *reinterpret_cast<const float4*>(all + 24 + r);
+          top[r] = max3(fmaxf(y0.x, y1.x), y2.x, y3.x);
+          top[r + 1] = max3(fmaxf(y0.y, y1.y), y2.y, y3.y);
+          top[r + 2] = max3(fmaxf(y0.z, y1.z), y2.z, y3.z);
+          top[r + 3] = max3(fmaxf(y0.w, y1.w), y2.w, y3.w);
         }
-        if (moved && t > 0) {  // the same on every thread of the group; PV(j - 1) may still add to O
-          if (!(ok = warp_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, a.status))) break;
-          tc_fence_after();
+        bool moved = false;
 #pragma unroll
-          for (int hf = 0; hf < C::HALVES; ++hf) {
-            float y[T][8];
+        for (int r = 0; r < 8; ++r) moved |= top[r] > m[r] + kMaxLead;
+        if (moved) {  // the same on every thread of the group
+          uint64_t corr[4];
 #pragma unroll
-            for (int u = 0; u < T; ++u) tmem_ld8(lane_base + C::COL_O + C::NB * hf + u * R + g8, y[u]);
+          for (int r = 0; r < 4; ++r) {
+            float c[2];
 #pragma unroll
-            for (int u = 0; u < T; ++u) tmem_ld8_wait(y[u]);
-#pragma unroll
-            for (int u = 0; u < T; ++u) {
-              uint32_t z[8];
-#pragma unroll
-              for (int r = 0; r < 8; ++r) z[r] = __float_as_uint(y[u][r] * corr[r]);
-              tmem_st8(lane_base + C::COL_O + C::NB * hf + u * R + g8, z);
+            for (int z = 0; z < 2; ++z) {
+              const float next = top[2 * r + z] > m[2 * r + z] + kMaxLead ? top[2 * r + z] : m[2 * r + z];
+              c[z] = ex2_approx(m[2 * r + z] - next);
+              m[2 * r + z] = next;
             }
+            corr[r] = f2_pack(c[0], c[1]);
+            l[r] = f2_mul(l[r], corr[r]);
           }
-          tmem_st_wait();
+          if (t > 0) {  // PV(j - 1) may still add to O
+            if (!(ok = warp_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, a.status))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int hf = 0; hf < C::HALVES; ++hf) {
+              float y[T][8];
+#pragma unroll
+              for (int u = 0; u < T; ++u) tmem_ld8(lane_base + C::COL_O + C::NB * hf + u * R + g8, y[u]);
+#pragma unroll
+              for (int u = 0; u < T; ++u) tmem_ld8_wait(y[u]);
+#pragma unroll
+              for (int u = 0; u < T; ++u) {
+                uint32_t z[8];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  float z0, z1;
+                  f2_unpack(f2_mul(f2_pack(y[u][2 * r], y[u][2 * r + 1]), corr[r]), z0, z1);
+                  z[2 * r] = __float_as_uint(z0);
+                  z[2 * r + 1] = __float_as_uint(z1);
+                }
+                tmem_st8(lane_base + C::COL_O + C::NB * hf + u * R + g8, z);
+              }
+            }
+            tmem_st_wait();
+          }
         }
 #pragma unroll
         for (int r = 0; r < 8; r += 2) {
-          const float p0 = ex2_approx(s[r] - (m[r] == neg_inf() ? 0.f : m[r]));
-          const float p1 = ex2_approx(s[r + 1] - (m[r + 1] == neg_inf() ? 0.f : m[r + 1]));
-          l[r] += p0;
-          l[r + 1] += p1;
+          float x0, x1;
+          f2_unpack(f2_add(s[r / 2], f2_pack(-m[r], -m[r + 1])), x0, x1);
+          const uint64_t p = f2_pack(ex2_approx(x0), ex2_approx(x1));
+          l[r / 2] = f2_add(l[r / 2], p);
           uint32_t code[T];
-          split_terms<T>(p0 * wv, p1 * wv, code);
-          // 128-byte swizzle: the 16-byte chunk is XORed with the row
-          const uint32_t at = p_row + i * C::P_BYTES + r * 128;
-          const uint32_t c0 = (chunk16 ^ r) << 4, c1 = (chunk16 ^ (r + 1)) << 4;
+          split_terms<T>(f2_mul(p, f2_pack(wv, wv)), code);
+          const uint32_t at = p_byte + i * C::P_BYTES;
 #pragma unroll
           for (int u = 0; u < T; ++u) {
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + c0 + u * R * 128), "r"(code[u] & 0xffu) : "memory");
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + c1 + u * R * 128 + 128), "r"(code[u] >> 8) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"((at ^ (r << 4)) + (u * R + r) * 128), "r"(code[u]) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"((at ^ ((r + 1) << 4)) + (u * R + r + 1) * 128),
+                         "r"(code[u] >> 8)
+                         : "memory");
           }
         }
         if (!live && g8 == 0) {  // no bytes of this slot may reach the product
@@ -865,11 +945,14 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
       }
       if (!ok) break;
       if (lane == 0) mbar_arrive(&seg_free[buf]);
+      queries(k + 1);
+      if (!ok) break;
       // l over the 128 slots of a tile: lanes, then warps
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const float y = warp_sum(l[r]);
-        if (lane == 0) my_sum[quarter * 8 + r] = y;
+      for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[r] = f2_add(l[r], __shfl_xor_sync(0xffffffffu, l[r], o));
+        if (lane == 0) *reinterpret_cast<uint64_t*>(my_sum + quarter * 8 + 2 * r) = l[r];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&my_exchange[x & 1]);
@@ -877,19 +960,24 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
       ++x;
       if (!(ok = warp_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, a.status))) break;
       tc_fence_after();
-      float inv[8];
+      uint64_t inv[4];
       const long long part_row = (long long)g.part * R + g8;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const float y = my_sum[r] + my_sum[8 + r] + my_sum[16 + r] + my_sum[24 + r];
-        inv[r] = y == 0.f ? 0.f : (1.f / kWeightScale) / y;
-        if (key == r && r < rows_here) {
-          const float lse2 = y == 0.f ? neg_inf() : (m[r] == neg_inf() ? 0.f : m[r]) + __log2f(y);
-          if (g.part < 0)
-            a.lse[out_row + r] = lse2 * kLn2;
-          else
-            a.lse_part[part_row + r] = lse2;
+      for (int r = 0; r < 8; r += 2) {
+        float v[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float y = my_sum[r + z] + my_sum[8 + r + z] + my_sum[16 + r + z] + my_sum[24 + r + z];
+          v[z] = y == 0.f ? 0.f : (1.f / kWeightScale) / y;
+          if (key == r + z && r + z < rows_here) {
+            const float lse2 = y == 0.f ? neg_inf() : m[r + z] + __log2f(y);
+            if (g.part < 0)
+              a.lse[out_row + r + z] = lse2 * kLn2;
+            else
+              a.lse_part[part_row + r + z] = lse2;
+          }
         }
+        inv[r / 2] = f2_pack(v[0], v[1]);
       }
 #pragma unroll
       for (int hf = 0; hf < C::HALVES; ++hf) {
@@ -898,13 +986,14 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
         for (int u = 0; u < T; ++u) tmem_ld8(lane_base + C::COL_O + C::NB * hf + u * R + g8, y[u]);
 #pragma unroll
         for (int u = 0; u < T; ++u) tmem_ld8_wait(y[u]);
+        uint64_t o[4];
+        join_terms<T>(y, o);
         const int f = hf * 128 + key;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          float z = y[T - 1][r];
-#pragma unroll
-          for (int u = T - 2; u >= 0; --u) z = fmaf(z, 0.0625f, y[u][r]);
-          z *= inv[r];
+          float z0, z1;
+          f2_unpack(f2_mul(o[r / 2], inv[r / 2]), z0, z1);
+          const float z = r & 1 ? z1 : z0;
           if (r < rows_here && f < D) {
             if (g.part >= 0) {
               a.o_part[(part_row + r) * D + f] = z;
