@@ -651,12 +651,17 @@ def forward_paged(cache, q, lens, causal=False, scale=None, weight_acc=None, max
     """Return (O, LSE) of q [B, Hq, Nq, d] over the 8-bit paged cache (arguments as fa_forward_paged)."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Nq, d]")
-    if workspace is None:
-        n = fa_paged_workspace_size(cache, q.shape[1], q.shape[2], max_len, num_splits, weight_acc is not None)
-        workspace = torch.empty(max(n, 1), device=q.device, dtype=torch.uint8)
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
-    fa_forward_paged(cache, q, lens, o, lse, workspace, causal, scale, weight_acc, max_len, num_splits, stream)
+    if stream is None:
+        on = torch.cuda.current_stream(cache.device)
+    else:
+        on = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), cache.device)
+    with torch.cuda.stream(on):  # what is allocated here belongs to the stream that uses it
+        if workspace is None:
+            n = fa_paged_workspace_size(cache, q.shape[1], q.shape[2], max_len, num_splits, weight_acc is not None)
+            workspace = torch.empty(max(n, 1), device=cache.device, dtype=torch.uint8)
+        o = torch.empty_like(q)
+        lse = torch.empty(q.shape[:3], device=cache.device, dtype=torch.float32)
+        fa_forward_paged(cache, q, lens, o, lse, workspace, causal, scale, weight_acc, max_len, num_splits, stream)
     return o, lse
 
 

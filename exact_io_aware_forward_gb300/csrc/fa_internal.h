@@ -11,7 +11,6 @@ namespace fa {
 // Status bits latched by kernels in the device status word.
 constexpr unsigned int kStatusTimeout = 1u;
 constexpr unsigned int kStatusBadSeqlens = 2u;  // a cu_seqlens range outside the packed tensors or maxima
-constexpr unsigned int kStatusBadPages = 4u;    // a page table entry outside the pool
 
 // The device status block: word 0 holds the kStatus* bits; words 2-3 and 4-5
 // are two 64-bit counters of the 64 x 64 (query x key) score blocks that the

@@ -812,8 +812,9 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
 #pragma unroll
           for (int r = 0; r < 4; r += 2) {
             const float4 q = *reinterpret_cast<const float4*>(qinv + 2 * r);
-            s[r] = f2_mul(f2_mul(s[r], f2_pack(q.x, q.y)), f2_pack(ks, ks));
-            s[r + 1] = f2_mul(f2_mul(s[r + 1], f2_pack(q.z, q.w)), f2_pack(ks, ks));
+            // the two scales first: a large one and a small one may meet
+            s[r] = f2_mul(s[r], f2_mul(f2_pack(q.x, q.y), f2_pack(ks, ks)));
+            s[r + 1] = f2_mul(s[r + 1], f2_mul(f2_pack(q.z, q.w), f2_pack(ks, ks)));
           }
         }
         if (!live || (g.first + t) * 128 + 128 > first_end) {
@@ -1048,27 +1049,32 @@ __device__ __forceinline__ Parts find_parts(const PagedAttnArgs& a, int bh, int 
 // sum[k] += sum over the rows, in order, of 2^(score - z[row]) for slots slot0 + 256 k; z = +inf: a row that sees
 // nothing (its scores are -inf).  W rows lie together, groups of W `stride` apart.
 template <int W, int SLOTS>
-__device__ __forceinline__ void add_weights(const float* from, long long stride, const float* z, int rows, int slot0,
-                                            int len, float (&sum)[SLOTS]) {
-  for (int g = 0; g < rows; g += W, from += stride) {
-    float y[SLOTS][W], ref[W];
+__device__ __forceinline__ void load_scores(const float* from, int slot0, int len, float (&y)[SLOTS][W]) {
 #pragma unroll
-    for (int k = 0; k < SLOTS; ++k)
-      if (slot0 + 256 * k < len) {
-        const float* at = from + (long long)(slot0 + 256 * k) * W;
-        if constexpr (W >= 4) {
+  for (int k = 0; k < SLOTS; ++k)
+    if (slot0 + 256 * k < len) {
+      const float* at = from + (long long)(slot0 + 256 * k) * W;
+      if constexpr (W >= 4) {
 #pragma unroll
-          for (int r = 0; r < W; r += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(at + r);
-            y[k][r] = v.x, y[k][r + 1] = v.y, y[k][r + 2] = v.z, y[k][r + 3] = v.w;
-          }
-        } else if constexpr (W == 2) {
-          const float2 v = *reinterpret_cast<const float2*>(at);
-          y[k][0] = v.x, y[k][1] = v.y;
-        } else {
-          y[k][0] = *at;
+        for (int r = 0; r < W; r += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(at + r);
+          y[k][r] = v.x, y[k][r + 1] = v.y, y[k][r + 2] = v.z, y[k][r + 3] = v.w;
         }
+      } else if constexpr (W == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(at);
+        y[k][0] = v.x, y[k][1] = v.y;
+      } else {
+        y[k][0] = *at;
       }
+    }
+}
+// `y` holds the first group's scores.
+template <int W, int SLOTS>
+__device__ __forceinline__ void add_weights(const float* from, long long stride, const float* z, int rows, int slot0,
+                                            int len, float (&y)[SLOTS][W], float (&sum)[SLOTS]) {
+  for (int g = 0; g < rows; g += W, from += stride) {
+    float ref[W];
+    if (g > 0) load_scores<W, SLOTS>(from, slot0, len, y);
 #pragma unroll
     for (int r = 0; r < W; ++r) ref[r] = g + r < rows ? z[g + r] : __int_as_float(0x7f800000);
 #pragma unroll
@@ -1193,6 +1199,9 @@ __global__ void __launch_bounds__(256, 5) paged_finish_kernel(const __grid_const
     for (int r0 = 0; r0 < a.rows; r0 += 64) {
       const int rows = min(64, a.rows - r0);
       if (r0 > 0) __syncthreads();
+      const float* from = a.scores + ((long long)bh * a.score_groups + r0 / 8) * a.score_stride;
+      float y[SLOTS][W];
+      load_scores<W, SLOTS>(from, slot0, len, y);  // under way while the rows' LSE are joined
       for (int r = warp; r < rows; r += 8) {  // a warp a row, its lanes the parts
         const int in_head = r0 + r;
         float m = neg_inf(), l = 0.f;
@@ -1214,8 +1223,7 @@ __global__ void __launch_bounds__(256, 5) paged_finish_kernel(const __grid_const
         if (lane == 0) s_z[r] = l == 0.f ? -neg_inf() : (m == neg_inf() ? 0.f : m) + __log2f(l);
       }
       __syncthreads();
-      const float* from = a.scores + ((long long)bh * a.score_groups + r0 / 8) * a.score_stride;
-      add_weights<W, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, sum);
+      add_weights<W, SLOTS>(from, a.score_stride, s_z, rows, slot0, len, y, sum);
     }
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k)
@@ -1227,11 +1235,14 @@ template <int D, int T, int G>
 cudaError_t launch_attention_t(const PagedAttnArgs& a, cudaStream_t stream) {
   using C = PagedCfg<D, T, G>;
   auto kern = paged_attention_kernel<D, T, G>;
+  // the same limit in every call: another thread may be about to launch with more pages
+  constexpr int kMostPages = kPagedMaxChunk / 16;
+  static_assert(C::smem(kMostPages) <= 232448, "shared memory budget");
+  if (a.seg_pages > kMostPages) return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(kMostPages));
+  if (e != cudaSuccess) return e;
   const int smem = C::smem(a.seg_pages);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
   const dim3 grid((unsigned)a.ctas, (unsigned)((a.rows + C::R - 1) / C::R));
   return launch_pdl(kern, grid, dim3(C::WARPS * 32), smem, stream, a);
 }
@@ -1300,7 +1311,9 @@ PagedPlan paged_plan(int B, int Hkv, int rows, int d, int ps, int max_len, int n
     p.ctas = ctas;
     p.splits = 1;
     p.per = 0;
-    const long long share = (all + ctas - 1) / ctas + 1;
+    // a piece of the line; where the lengths leave less than this, pieces of at most min_tiles
+    long long share = (all + ctas - 1) / ctas + 1;
+    if (share < p.min_tiles) share = p.min_tiles;
     segment = (int)(share < tiles ? share : tiles);
     p.parts = 2 * ctas * row_tiles;
   } else {

@@ -19,6 +19,9 @@ struct PagedView {
   bool e5m2 = false;
 };
 
+// Status bit (beside those of fa_internal.h): a page table entry outside the pool.
+constexpr unsigned int kStatusBadPages = 4u;
+
 // Slots of one segment of attention: what can be lost of tiny weights grows
 // with it, and its page list sits in shared memory.
 constexpr int kPagedMaxChunk = 16384;
