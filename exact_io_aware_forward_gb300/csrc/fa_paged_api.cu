@@ -23,7 +23,7 @@ fa_status check_cache(const fa_paged_cache* c) {
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return FA_ERR_UNSUPPORTED;
   if (c->cache_dtype != FA_E4M3 && c->cache_dtype != FA_E5M2) return FA_ERR_UNSUPPORTED;
-  if ((long long)c->num_pages * c->Hkv >= (1LL << 31) || (long long)c->pages_per_seq * c->page_size >= (1LL << 31) ||
+  if ((long long)c->num_pages * c->Hkv >= (1LL << 31) || (long long)c->pages_per_seq * c->page_size > (1LL << 30) ||
       (long long)c->B * c->Hkv > 65535 || c->Hkv > 32767)
     return FA_ERR_UNSUPPORTED;
   return FA_OK;

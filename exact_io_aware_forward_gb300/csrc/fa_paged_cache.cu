@@ -260,115 +260,89 @@ __device__ __forceinline__ void store_remote(const void* mine, uint32_t rank, in
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
 }
 
-struct Three {
-  int a, b, c;
+__device__ __forceinline__ int load_remote(const void* mine, uint32_t rank) {
+  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine)), there;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
+  return v;
+}
+template <int C>
+__device__ __forceinline__ void all_sync() {
+  if (C > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+}
+
+struct Pair {
+  int a, b;
 };
-// Sums over the threads of the C CTAs of a cluster (TH threads each), for every thread.
+// Exclusive prefix sums of two numbers over all threads of the C CTAs of a
+// cluster (TH threads each), in order, and their totals.  s_warp: 32 pairs; s_cta:
+// 8 pairs, used for one call only.
 template <int C, int TH>
-struct Gather {
-  unsigned (*s_sum)[3];       // [kTurns] zeros
-  int (*s_warp)[2];           // [32]
-  int (*s_cta)[8][3];         // [2] turns
-  int turn = 0;
-  static constexpr int kTurns = 24;
-  // Numbers of at most 20 a thread are added up three in a word, in one
-  // reduction of the warp; larger ones (runs too long for registers) one by one.
-  __device__ __forceinline__ Three sum(Three v, bool small) {
-    const int lane = threadIdx.x & 31;
-    unsigned* at = s_sum[turn];
-    if (small) {
-      const unsigned x = __reduce_add_sync(0xffffffffu, (unsigned)v.a | (unsigned)v.b << 10 | (unsigned)v.c << 20);
-      if (lane == 0) atomicAdd(at, (x & 1023u) | (x >> 10 & 1023u) << 16);  // at most 20 * 1024 each
-      if (lane == 1) atomicAdd(at + 2, x >> 20);
-    } else {
-      v.a = __reduce_add_sync(0xffffffffu, v.a);
-      v.b = __reduce_add_sync(0xffffffffu, v.b);
-      v.c = __reduce_add_sync(0xffffffffu, v.c);
-      if (lane < 3) atomicAdd(at + lane, (unsigned)(lane == 0 ? v.a : lane == 1 ? v.b : v.c));
-    }
-    __syncthreads();
-    v.a = (int)(small ? at[0] & 0xffffu : at[0]);
-    v.b = (int)(small ? at[0] >> 16 : at[1]);
-    v.c = (int)at[2];
-    if (C > 1) {
-      int(*all)[3] = s_cta[turn & 1];
-      int* mine = all[cluster_rank()];
-      if (threadIdx.x < 3 * C) {
-        const int i = threadIdx.x % 3;
-        store_remote(mine + i, threadIdx.x / 3, i == 0 ? v.a : i == 1 ? v.b : v.c);
-      }
-      cluster_sync();
-      v.a = v.b = v.c = 0;
+__device__ __forceinline__ Pair sum_before(Pair v, int (*s_warp)[2], int (*s_cta)[2], Pair* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int x = v.a, y = v.b;
 #pragma unroll
-      for (int r = 0; r < C; ++r) {
-        v.a += all[r][0];
-        v.b += all[r][1];
-        v.c += all[r][2];
-      }
-    }
-    ++turn;
-    return v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) x += p, y += q;
   }
-  // Exclusive prefix sums of a and b over all threads of the cluster, in order.
-  __device__ __forceinline__ Three before(Three v, Three* total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int x = v.a, y = v.b;
+  __syncthreads();  // the list may still be read from the call before
+  if (lane == 31) s_warp[warp][0] = x, s_warp[warp][1] = y;
+  __syncthreads();
+  const int wa = lane < TH / 32 ? s_warp[lane][0] : 0, wb = lane < TH / 32 ? s_warp[lane][1] : 0;
+  Pair r, all;
+  r.a = x - v.a + __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);
+  r.b = y - v.b + __reduce_add_sync(0xffffffffu, lane < warp ? wb : 0);
+  all.a = __reduce_add_sync(0xffffffffu, wa);
+  all.b = __reduce_add_sync(0xffffffffu, wb);
+  if (C > 1) {
+    const int rank = (int)cluster_rank();
+    if (threadIdx.x < 2 * C)
+      store_remote(s_cta[rank] + (threadIdx.x & 1), threadIdx.x >> 1, threadIdx.x & 1 ? all.b : all.a);
+    cluster_sync();
+    all.a = all.b = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) x += p, y += q;
+    for (int c = 0; c < C; ++c) {
+      if (c < rank) r.a += s_cta[c][0], r.b += s_cta[c][1];
+      all.a += s_cta[c][0];
+      all.b += s_cta[c][1];
     }
-    __syncthreads();  // the list may still be read from the call before
-    if (lane == 31) s_warp[warp][0] = x, s_warp[warp][1] = y;
-    __syncthreads();
-    const int wa = lane < TH / 32 ? s_warp[lane][0] : 0, wb = lane < TH / 32 ? s_warp[lane][1] : 0;
-    Three r, all;
-    r.a = x - v.a + __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);
-    r.b = y - v.b + __reduce_add_sync(0xffffffffu, lane < warp ? wb : 0);
-    all.a = __reduce_add_sync(0xffffffffu, wa);
-    all.b = __reduce_add_sync(0xffffffffu, wb);
-    r.c = all.c = 0;
-    if (C > 1) {
-      const int rank = (int)cluster_rank();
-      int(*of)[3] = s_cta[turn & 1];
-      if (threadIdx.x < 2 * C) store_remote(of[rank] + (threadIdx.x & 1), threadIdx.x >> 1, threadIdx.x & 1 ? all.b : all.a);
-      cluster_sync();
-      all.a = all.b = 0;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (c < rank) r.a += of[c][0], r.b += of[c][1];
-        all.a += of[c][0];
-        all.b += of[c][1];
-      }
-    }
-    ++turn;
-    *total = all;
-    return r;
   }
-};
+  *total = all;
+  return r;
+}
 
 // One cluster of C CTAs a (sequence, head): which slots leave, and which of the
 // kept ones move where.  A thread owns a run of consecutive slots, its keys
-// in registers (up to 20; longer runs are read again in every pass).  The
-// m-th largest key is found two bits at a time (three counts a step over all
-// keys), at most 16 steps whatever the distribution, fewer where a count
-// meets m earlier, and no atomics on data.  Equal keys: the lowest slots stay.
-// Prefix sums over the runs then give every hole and every mover its place in
-// slot order.  Reads 8 bytes a slot; the steps are bound by their barriers
-// and by the reductions, so small CTAs and one reduction a step (2080 slots
-// for 32 x 8 heads: 27 us with 1024 threads and three reductions).
+// in registers (up to 20; longer runs are read again in every pass).
+//
+// The m-th largest key lies in a window [lo, hi], at first from the smallest
+// to the largest key that is not protected.  A pass sorts the window's keys
+// into 256 bins of equal width, adds the bins up from the top, and the bin
+// where the sum reaches m is the next window: at most four passes, fewer where
+// a window's keys all stay.  The bins are integers: no order of additions
+// changes them.  (Finding the key two bits at a time by counting took up to 16
+// passes: 23 us for 64 heads of 16384 slots, 10.5 us for 256 heads of 2080.)
+// Equal keys: the lowest slots stay.  Prefix sums over the runs then give every
+// hole and every mover its place in slot order.  Reads 8 bytes a slot.
 template <int C, int TH>
 __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant__ PagedEvictArgs a) {
   constexpr int K = kSelectKeys;
-  using Sums = Gather<C, TH>;
-  __shared__ unsigned s_sum[Sums::kTurns][3];
-  __shared__ int s_warp[32][2];
-  __shared__ int s_cta[2][8][3];
+  __shared__ int s_bin[2][256];  // two passes' turns
+  __shared__ unsigned s_red[32][4];
+  __shared__ unsigned s_cta[8][4];
+  __shared__ int s_warp[32][2], s_before[2][8][2];
+  __shared__ int s_pick[2][3];
   const int bh = blockIdx.x / C, b = bh / a.c.Hkv, h = bh % a.c.Hkv;
   const int rank = C > 1 ? (int)cluster_rank() : 0;
-  const int tid = threadIdx.x, ps = a.c.ps;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ps = a.c.ps;
   const bool speaks = rank == 0 && tid == 0;
   pdl_launch();
+  if (tid < 256) s_bin[0][tid] = s_bin[1][tid] = 0;
   pdl_wait();
   const int n = a.lens[b];
   if (n < 0 || n > a.c.width * ps || n <= a.keep) {  // the same for the whole cluster
@@ -387,16 +361,11 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
   const float* weight = a.weight_acc + state;
   const int* position = a.positions + state;
   // runs of a multiple of four slots
-  const int run = ((n + TH * C - 1) / (TH * C) + 3) & ~3;
+  const int run = (int)(((n + TH * C - 1LL) / (TH * C) + 3) & ~3LL);
   const long long begin = (long long)(rank * TH + tid) * run;
-  const int s0 = (int)(begin < n ? begin : n), s1 = min(n, s0 + run);
+  const int s0 = (int)(begin < n ? begin : n), s1 = (int)(s0 + (long long)run < n ? s0 + run : n);
   const bool cached = run <= K;
-  Sums gather = {s_sum, s_warp, s_cta};
-  if (tid < 3 * Sums::kTurns) s_sum[tid / 3][tid % 3] = 0;
-  if (C > 1) cluster_sync();  // all CTAs of the cluster are there
-  else __syncthreads();
 
-  int latest = INT_MIN, bad = 0;
   // four slots' weights and positions (0 and the lowest number where there is none)
   auto load4 = [&](int s, float (&w)[4], int (&p)[4]) {
     if (s + 4 <= s1) {
@@ -412,6 +381,8 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
       }
     }
   };
+  // the largest position, and whether a page is bad
+  int latest = INT_MIN, bad = 0;
   for (int s = s0; s < s1; s += 4) {
     float w[4];
     int p[4];
@@ -420,19 +391,23 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
   }
   for (int t = rank * TH + tid; t < (n + ps - 1) / ps; t += TH * C)
     bad |= table[t] < 0 || table[t] >= a.c.pages;
-  {  // the largest position
-    latest = __reduce_max_sync(0xffffffffu, latest);
-    if ((tid & 31) == 0) s_warp[tid >> 5][0] = latest;
-    __syncthreads();
-    latest = __reduce_max_sync(0xffffffffu, s_warp[tid & (TH / 32 - 1)][0]);
-    if (C > 1) {
-      if (tid < C) store_remote(s_cta[1][rank], tid, latest);
-      cluster_sync();
+  latest = __reduce_max_sync(0xffffffffu, latest);
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) s_red[warp][0] = (unsigned)latest, s_red[warp][1] = bad;
+  __syncthreads();
+  latest = __reduce_max_sync(0xffffffffu, (int)s_red[lane & (TH / 32 - 1)][0]);
+  bad = __any_sync(0xffffffffu, s_red[lane & (TH / 32 - 1)][1]);
+  if (C > 1) {
+    cluster_sync();  // all CTAs of the cluster are there
+    if (tid < 2 * C) store_remote(&s_cta[rank][tid & 1], tid >> 1, tid & 1 ? bad : latest);
+    cluster_sync();
 #pragma unroll
-      for (int r = 0; r < C; ++r) latest = max(latest, s_cta[1][r][0]);
+    for (int r = 0; r < C; ++r) {
+      latest = max(latest, (int)s_cta[r][0]);
+      bad |= (int)s_cta[r][1];
     }
   }
-  if (gather.sum({bad, 0, 0}, true).a) {  // reported; the sequence stays as it is (every head sees the same row)
+  if (bad) {  // reported; the sequence stays as it is (every head sees the same row)
     if (speaks) {
       if (h == 0) {
         atomicOr(a.status, kStatusBadPages);
@@ -440,6 +415,7 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
       }
       a.plan_count[bh] = 0;
     }
+    if (C > 1) cluster_sync();  // no CTA leaves while another may still write to its shared memory
     return;
   }
   uint32_t key[K];
@@ -456,93 +432,133 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
     }
   }
   auto key_at = [&](int s) { return rank_key(weight[s], position[s], latest, a.recent); };
-
-  // The largest v with at least m keys >= v (keys of slots are at least 0x007fffff, 0 is none).
-  uint32_t v = 0;
-  int at_least = n;  // keys >= v
-  for (int step = 0; step < 16 && at_least != m; ++step) {
-    const int shift = 30 - 2 * step;
-    const uint32_t t1 = v | (1u << shift), t2 = v | (2u << shift), t3 = v | (3u << shift);
-    Three c = {0, 0, 0};
-    if (cached) {
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        if (i >= run) break;  // the same for all threads
-        c.a += key[i] >= t1;
-        c.b += key[i] >= t2;
-        c.c += key[i] >= t3;
-      }
-    } else {
-      for (int s = s0; s < s1; ++s) {
-        const uint32_t k = key_at(s);
-        c.a += k >= t1;
-        c.b += k >= t2;
-        c.c += k >= t3;
-      }
-    }
-    c = gather.sum(c, cached);
-    if (c.c >= m) v = t3, at_least = c.c;
-    else if (c.b >= m) v = t2, at_least = c.b;
-    else if (c.a >= m) v = t1, at_least = c.a;
-  }
-  // Of the keys equal to v all stay (at_least = m), or the first m - above.
-  int stay = INT_MAX, eq = 0;
-  if (at_least != m) {
-    Three mine = {0, 0, 0}, all;
-    if (cached) {
-#pragma unroll
-      for (int i = 0; i < K; ++i) mine.a += key[i] > v, mine.b += key[i] == v;
-    } else {
-      for (int s = s0; s < s1; ++s) {
-        const uint32_t k = key_at(s);
-        mine.a += k > v, mine.b += k == v;
-      }
-    }
-    eq = gather.before(mine, &all).b;
-    stay = m - all.a;
-  }
-  auto kept = [&](uint32_t k, int& e) {
-    const bool yes = k > v || (k == v && e < stay);
-    e += k == v;
-    return yes;
-  };
-  Three mine = {0, 0, 0}, all;
-  {
-    int e = eq;
+  // f(key, slot) for every slot of the run
+  auto each = [&](auto f) {
     if (cached) {
 #pragma unroll
       for (int i = 0; i < K; ++i)
-        if (i < run && s0 + i < s1) {
-          const bool yes = kept(key[i], e);
-          mine.a += !yes && s0 + i < m;
-          mine.b += yes && s0 + i >= m;
-        }
+        if (i < run && s0 + i < s1) f(key[i], s0 + i);
     } else {
-      for (int s = s0; s < s1; ++s) {
-        const bool yes = kept(key_at(s), e);
-        mine.a += !yes && s < m;
-        mine.b += yes && s >= m;
-      }
+      for (int s = s0; s < s1; ++s) f(key_at(s), s);
+    }
+  };
+
+  // the smallest key, the largest that is not protected, the protected ones
+  uint32_t lo = 0xffffffffu, hi = 0;
+  unsigned shielded = 0;
+  each([&](uint32_t k, int) {
+    lo = min(lo, k);
+    if (k != 0xffffffffu) hi = max(hi, k);
+    else ++shielded;
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  shielded = __reduce_add_sync(0xffffffffu, shielded);
+  __syncthreads();  // s_red has been read
+  if (lane == 0) s_red[warp][0] = lo, s_red[warp][1] = hi, s_red[warp][2] = shielded;
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, s_red[lane & (TH / 32 - 1)][0]);
+  hi = __reduce_max_sync(0xffffffffu, s_red[lane & (TH / 32 - 1)][1]);
+  shielded = __reduce_add_sync(0xffffffffu, lane < TH / 32 ? s_red[lane][2] : 0u);
+  if (C > 1) {
+    cluster_sync();  // s_cta has been read
+    if (tid < 3 * C) {
+      const int i = tid % 3;
+      store_remote(&s_cta[rank][i], tid / 3, (int)(i == 0 ? lo : i == 1 ? hi : shielded));
+    }
+    cluster_sync();
+    shielded = 0;
+#pragma unroll
+    for (int r = 0; r < C; ++r) {
+      lo = min(lo, s_cta[r][0]);
+      hi = max(hi, s_cta[r][1]);
+      shielded += s_cta[r][2];
     }
   }
-  const Three from = gather.before(mine, &all);
+  int above = (int)shielded, in = n - above;  // keys over the window, and in it
+  if (above >= m) lo = hi = 0xffffffffu, in = above, above = 0;
+  for (int pass = 0; in != m - above && lo != hi; ++pass) {
+    const int turn = pass & 1;
+    const int shift = max(0, 24 - __clz(hi - lo));  // at most 256 bins
+    int* bin = s_bin[turn];
+    each([&](uint32_t k, int) {
+      if (k >= lo && k <= hi) {
+        const uint32_t at = (k - lo) >> shift;
+        // many equal weights: one addition for all lanes that are here
+        const unsigned lanes = __activemask();
+        int same;
+        __match_all_sync(lanes, at, &same);
+        if (!same) atomicAdd(bin + at, 1);
+        else if ((threadIdx.x & 31) == (unsigned)(__ffs(lanes) - 1)) atomicAdd(bin + at, __popc(lanes));
+      }
+    });
+    all_sync<C>();
+    // sums from the top, a bin a thread
+    int mine = 0, sum = 0;
+    if (tid < 256) {
+      mine = bin[tid];
+      if (C > 1) {
+        mine = 0;
+#pragma unroll
+        for (int r = 0; r < C; ++r) mine += load_remote(bin + tid, r);
+      }
+      sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += y;
+      }
+      if (lane == 0) s_warp[warp][0] = sum;
+    }
+    __syncthreads();
+    if (tid < 256) {
+      for (int w = warp + 1; w < 8; ++w) sum += s_warp[w][0];
+      if (sum >= m - above && sum - mine < m - above) {
+        s_pick[turn][0] = tid;
+        s_pick[turn][1] = sum - mine;
+        s_pick[turn][2] = mine;
+      }
+      s_bin[turn ^ 1][tid] = 0;  // the other turn's bins have been read by all CTAs before this pass's all_sync
+    }
+    __syncthreads();
+    lo += (uint32_t)s_pick[turn][0] << shift;
+    hi = min(hi, lo + ((1u << shift) - 1u));
+    above += s_pick[turn][1];
+    in = s_pick[turn][2];
+  }
+  // Of the window's keys all stay, or (equal ones) the first m - above.
+  const int stay = in == m - above ? INT_MAX : m - above;
+  int eq = 0;
+  if (stay != INT_MAX) {
+    Pair mine = {0, 0}, all;
+    each([&](uint32_t k, int) { mine.a += k == lo; });
+    eq = sum_before<C, TH>(mine, s_warp, s_before[0], &all).a;
+  }
+  auto kept = [&](uint32_t k, int& e) {
+    const bool yes = k > lo || (k == lo && e < stay);
+    e += k == lo;
+    return yes;
+  };
+  Pair mine = {0, 0}, all;
+  {
+    int e = eq;
+    each([&](uint32_t k, int s) {
+      const bool yes = kept(k, e);
+      mine.a += !yes && s < m;
+      mine.b += yes && s >= m;
+    });
+  }
+  const Pair from = sum_before<C, TH>(mine, s_warp, s_before[1], &all);
   const long long list = (long long)bh * m;
   const int pages = (m + ps - 1) / ps;
   int* page_holes = a.page_holes + (long long)bh * (pages + 1);  // holes before each page
   int hole_at = from.a, mover_at = from.b;
-  auto put = [&](int s, uint32_t k) {
+  each([&](uint32_t k, int s) {
     const bool yes = kept(k, eq);
     if (s < m && (s & (ps - 1)) == 0) page_holes[s >> a.c.ps_shift] = hole_at;
     if (!yes && s < m) a.holes[list + hole_at++] = s;
     if (yes && s >= m) a.movers[list + mover_at++] = s;
-  };
-  if (cached) {
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-      if (i < run && s0 + i < s1) put(s0 + i, key[i]);
-  } else {
-    for (int s = s0; s < s1; ++s) put(s, key_at(s));
-  }
+  });
   if (speaks) {
     page_holes[pages] = all.a;
     a.plan_count[bh] = all.a;
@@ -552,7 +568,7 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
       a.edge_scales[bh] = make_float2(a.c.k_scale[at], a.c.v_scale[at]);
     }
   }
-  if (C > 1) cluster_sync();  // no CTA leaves while another may still write to its shared memory
+  if (C > 1) cluster_sync();  // no CTA leaves while another may still use its shared memory
 }
 
 // One warp a (page before the new length, sequence and head): the movers that
@@ -683,9 +699,8 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, cudaStream_t stream) {
   // One CTA of 256 threads a head where its slots' keys fit in its registers
-  // (5120), else 1024 threads, else a cluster of those: a step of the search
-  // costs 0.5 us in a CTA and 1.25 us in a cluster (its barriers), which was
-  // more than eight CTAs of 256 threads gained on a head of 16384 slots.
+  // (5120), else 1024 threads, else a cluster of those (every barrier of a
+  // cluster costs about 0.7 us).
   const int BH = a.c.B * a.c.Hkv;
   const long long slots = (long long)a.c.width * a.c.ps;
   const bool small = slots <= 256 * kSelectKeys;

@@ -394,8 +394,8 @@ fa_status fa_forward_decode_gqa(const void* q, const void* k, const void* v, voi
  * slot t of sequence b is row t % page_size of page
  * page_table[b][t / page_size].  All are device pointers, 16-byte aligned;
  * the struct itself lives on the host and is read during the call only.
- * page_size in {16, 32, 64, 128}, d in {64, 128, 256}, num_pages * Hkv and
- * pages_per_seq * page_size < 2^31, B * Hkv <= 65535, Hkv <= 32767.
+ * page_size in {16, 32, 64, 128}, d in {64, 128, 256}, num_pages * Hkv < 2^31,
+ * pages_per_seq * page_size <= 2^30, B * Hkv <= 65535, Hkv <= 32767.
  *
  * The filled slots of sequence b are 0 .. lens[b] - 1 (`lens`: [B] device
  * int32, read on the device).  Calls that change the number of slots write

@@ -428,17 +428,38 @@ def test_evict_odd_weights():
             assert np.array_equal(x, y, equal_nan=x.dtype.kind == "f"), name
 
 
-def test_evict_more_slots_than_fit_on_chip():
-    """60000 slots: the keys no longer fit in shared memory."""
-    c = Cache(1, 1, 469, 128, 64, seed=70)
+@pytest.mark.parametrize("n,ps,kind", [(20400, 16, "many"), (60000, 128, "many"), (60000, 128, "few"),
+                                       (170000, 128, "many"), (40000, 64, "zeros")])
+def test_evict_long_heads(n, ps, kind):
+    """Heads that take one large CTA, a cluster, and more than a cluster holds in registers; many different
+    weights, a few, mostly zeros."""
+    T = (n + ps - 1) // ps + 1
+    c = Cache(1, 1, T, ps, 64, seed=70)
     rng = np.random.default_rng(71)
-    w = rng.integers(0, 3000, (1, 1, 469 * 128)).astype(np.float32)
-    pos = np.arange(469 * 128, dtype=np.int32).reshape(1, 1, -1)
-    acc, position, new_lens = _run_evict(c, w, pos, [60000], 20001, 700)
+    w = rng.integers(0, 3 if kind == "few" else 30000, (1, 1, T * ps)).astype(np.float32)
+    if kind == "zeros":
+        w *= rng.random(w.shape) < 0.1
+    pos = np.arange(T * ps, dtype=np.int32).reshape(1, 1, -1)
+    keep = n // 3 + 1
+    acc, position, new_lens = _run_evict(c, w, pos, [n], keep, 700)
     fa.fa_device_status()
-    want = P.evict(c.np, "e4m3", c.table, w, pos, np.array([60000]), 20001, 700)
+    want = P.evict(c.np, "e4m3", c.table, w, pos, np.array([n]), keep, 700)
     got = c.read() + [acc.cpu().numpy(), position.cpu().numpy(), new_lens.cpu().numpy()]
     assert all(np.array_equal(x, y) for x, y in zip(got, want))
+
+
+def test_evict_when_all_weights_are_equal():
+    for value in (0.0, -0.0, np.inf, np.nan, -3.0):
+        c = Cache(2, 1, 10, 64, 64, seed=72)
+        w = np.full((2, 1, 640), value, np.float32)
+        pos = np.zeros((2, 1, 640), np.int32)
+        pos[:, :, 600:] = 9
+        for recent in (0, 5):
+            acc, position, new_lens = _run_evict(c, w, pos, [640, 500], 321, recent)
+            fa.fa_device_status()
+            want = P.evict(c.np, "e4m3", c.table, w, pos, np.array([640, 500]), 321, recent)
+            got = c.read() + [acc.cpu().numpy(), position.cpu().numpy(), new_lens.cpu().numpy()]
+            assert all(np.array_equal(x, y, equal_nan=x.dtype.kind == "f") for x, y in zip(got, want)), (value, recent)
 
 
 def test_evict_refuses_on_the_device():
