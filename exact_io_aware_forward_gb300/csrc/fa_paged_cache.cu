@@ -86,7 +86,8 @@ __device__ __forceinline__ float scale_for(float amax) {
 }
 
 // ---------------------------------------------------------------- append
-// One CTA a (sequence, page, head, K or V): the page's new rows are read
+// One CTA (or, WARP, one warp: pages with at most 2048 new elements, eight to
+// a CTA) a (sequence, page, head, K or V): the page's new rows are read
 // once (16 elements a thread and step, kept in registers), their maximum
 // gives the scale, and they are written as codes.  Reads 2 and writes 1
 // byte an element.  A prompt is bound by memory as long as an element costs
@@ -94,56 +95,68 @@ __device__ __forceinline__ float scale_for(float amax) {
 // time, and infinities and NaN are looked at one by one only in pages that
 // have some (8192 tokens for 4 x 8 heads: 46 us with every element looked at).
 // One token a sequence is bound by the launch and three dependent reads.
-template <bool E5M2, int NV>
-__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+template <bool E5M2, int NV, bool WARP>
+__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int reach) {
   pdl_launch();
   pdl_wait();
-  const int b = blockIdx.z, h = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
+  int x, y, b;  // page among those that may be reached, head and K or V, sequence
+  if (WARP) {
+    const long long item = blockIdx.x * 8LL + (threadIdx.x >> 5);
+    x = (int)(item % reach);
+    const long long rest = item / reach;
+    if (rest >= 2LL * a.c.Hkv * a.c.B) return;
+    y = (int)(rest % (2 * a.c.Hkv));
+    b = (int)(rest / (2 * a.c.Hkv));
+  } else {
+    x = blockIdx.x, y = blockIdx.y, b = blockIdx.z;
+  }
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+  const int h = y >> 1;
+  const bool is_v = y & 1;
   const int ps = a.c.ps, d = a.c.d;
   const int len = a.lens[b];
   const int cnt = a.counts ? a.counts[b] : a.N;
-  const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
+  const bool first = x == 0 && y == 0;
   if (len < 0 || cnt < 0 || cnt > a.N || len > a.c.width * ps || cnt > a.c.width * ps - len) {
-    if (first_cta && threadIdx.x == 0) {
+    if (first && tid == 0) {
       atomicOr(a.status, kStatusBadSeqlens);
       a.new_lens[b] = len;
     }
     return;
   }
-  if (first_cta && threadIdx.x == 0) a.new_lens[b] = len + cnt;
-  const int t = (len >> a.c.ps_shift) + blockIdx.x;
+  if (first && tid == 0) a.new_lens[b] = len + cnt;
+  const int t = (len >> a.c.ps_shift) + x;
   const int start = t * ps;
   const int lo = max(len, start), hi = min(len + cnt, start + ps);
   if (lo >= hi) return;
   const int page = a.c.table[(long long)b * a.c.width + t];
-  const uint16_t* x = static_cast<const uint16_t*>(is_v ? a.v : a.k) +
+  const uint16_t* from = static_cast<const uint16_t*>(is_v ? a.v : a.k) +
                       (((long long)b * a.c.Hkv + h) * a.N + (lo - len)) * d;
   const int vecs = (hi - lo) * d / 16;
   uint4 in[NV][2];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = i * blockDim.x + threadIdx.x;
+    const int e = i * threads + tid;
     if (e < vecs) {
-      in[i][0] = __ldcs(reinterpret_cast<const uint4*>(x) + 2 * e);
-      in[i][1] = __ldcs(reinterpret_cast<const uint4*>(x) + 2 * e + 1);
+      in[i][0] = __ldcs(reinterpret_cast<const uint4*>(from) + 2 * e);
+      in[i][1] = __ldcs(reinterpret_cast<const uint4*>(from) + 2 * e + 1);
     } else {
       in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
     }
   }
   const long long state = ((long long)b * a.c.Hkv + h) * a.c.width * ps;
   if (!is_v) {  // bookkeeping of the new slots
-    for (int s = lo + threadIdx.x; s < hi; s += blockDim.x) {
+    for (int s = lo + tid; s < hi; s += threads) {
       if (a.weight_acc) a.weight_acc[state + s] = 0.f;
       if (a.positions) a.positions[state + s] = (a.first_position ? a.first_position[b] : len) + (s - len);
     }
   }
   if (page < 0 || page >= a.c.pages) {
-    if (threadIdx.x == 0) atomicOr(a.status, kStatusBadPages);
+    if (tid == 0) atomicOr(a.status, kStatusBadPages);
     return;
   }
   float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + (long long)page * a.c.Hkv + h;
-  const float was = lo > start ? *scale : 0.f;  // read by every thread before the barrier, written after it
+  const float was = lo > start ? *scale : 0.f;  // read by every thread before it is written
   auto word = [&](int i, int w) {
     const uint4& u = in[i][w >> 2];
     return (w & 3) == 0 ? u.x : (w & 3) == 1 ? u.y : (w & 3) == 2 ? u.z : u.w;
@@ -155,12 +168,16 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int w = 0; w < 8; ++w) two = __vmaxu2(two, word(i, w) & 0x7fff7fffu);
-  __shared__ uint32_t s_top[8], s_fin[8];
-  const uint32_t mine = __reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16));
-  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = mine;
-  __syncthreads();
-  uint32_t top = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) top = max(top, s_top[w]);
+  __shared__ uint32_t s_top[2][8];
+  auto most = [&](uint32_t mine, int turn) {
+    mine = __reduce_max_sync(0xffffffffu, mine);
+    if (WARP) return mine;
+    if ((tid & 31) == 0) s_top[turn][tid >> 5] = mine;
+    __syncthreads();
+    for (int w = 0; w < (int)(threads >> 5); ++w) mine = max(mine, s_top[turn][w]);
+    return mine;
+  };
+  uint32_t top = most(max(two & 0xffffu, two >> 16), 0);
   const bool all_finite = top < inf16;
   if (!all_finite) {  // infinities and NaN do not set the scale
     uint32_t fin = 0;
@@ -172,18 +189,14 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
         if ((m & 0xffffu) < inf16) fin = max(fin, m & 0xffffu);
         if ((m >> 16) < inf16) fin = max(fin, m >> 16);
       }
-    fin = __reduce_max_sync(0xffffffffu, fin);
-    if ((threadIdx.x & 31) == 0) s_fin[threadIdx.x >> 5] = fin;
-    __syncthreads();
-    top = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) top = max(top, s_fin[w]);
+    top = most(fin, 1);
   }
   const float now = fmaxf(was, scale_for<E5M2>(unpack16(top, a.bf16).x));
   uint8_t* codes = (is_v ? a.c.v_pages : a.c.k_pages) + ((long long)page * a.c.Hkv + h) * ps * d;
   if (lo > start && now != was) {  // the slots that were there, at the larger scale
     const float ratio = was / now;
     uint4* old = reinterpret_cast<uint4*>(codes);
-    for (int e = threadIdx.x; e < (lo - start) * d / 16; e += blockDim.x) old[e] = rescale16<E5M2>(old[e], ratio);
+    for (int e = tid; e < (lo - start) * d / 16; e += threads) old[e] = rescale16<E5M2>(old[e], ratio);
   }
   // x / now; for a power of two the product with its inverse is the same number
   const bool power = (__float_as_uint(now) & 0x7fffffu) == 0 && now >= 0x1p-126f && now <= 0x1p126f;
@@ -192,7 +205,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
   uint4* out = reinterpret_cast<uint4*>(codes + (long long)(lo - start) * d);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = i * blockDim.x + threadIdx.x;
+    const int e = i * threads + tid;
     if (e >= vecs) break;
     uint32_t half[8];
     if (plain) {
@@ -213,21 +226,26 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
     out[e] = make_uint4(half[0] | half[1] << 16, half[2] | half[3] << 16, half[4] | half[5] << 16,
                         half[6] | half[7] << 16);
   }
-  if (threadIdx.x == 0 && now != was) *scale = now;
+  if (WARP) __syncwarp();
+  if (tid == 0 && now != was) *scale = now;
 }
 
 template <bool E5M2>
 cudaError_t launch_append_t(const PagedAppendArgs& a, cudaStream_t stream) {
-  const int vecs = a.c.ps * a.c.d / 16;  // of a full page: 64 to 2048
-  const int threads = vecs < 256 ? vecs : 256;
   // pages that N tokens can reach, wherever the first of them lands
   const int reach = (int)((a.N + a.c.ps - 2LL) / a.c.ps + 1);
+  const long long items = 2LL * reach * a.c.Hkv * a.c.B;
+  if ((a.N < a.c.ps ? a.N : a.c.ps) * a.c.d <= 2048 && items <= 8LL * 0x7fffffff)
+    return launch_pdl(paged_append_kernel<E5M2, 4, true>, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, stream, a,
+                      reach);
+  const int vecs = a.c.ps * a.c.d / 16;  // of a full page: 64 to 2048
+  const int threads = vecs < 256 ? vecs : 256;
   const dim3 grid((unsigned)reach, (unsigned)(2 * a.c.Hkv), (unsigned)a.c.B);
   switch (vecs / threads) {
-    case 1: return launch_pdl(paged_append_kernel<E5M2, 1>, grid, dim3(threads), 0, stream, a);
-    case 2: return launch_pdl(paged_append_kernel<E5M2, 2>, grid, dim3(threads), 0, stream, a);
-    case 4: return launch_pdl(paged_append_kernel<E5M2, 4>, grid, dim3(threads), 0, stream, a);
-    case 8: return launch_pdl(paged_append_kernel<E5M2, 8>, grid, dim3(threads), 0, stream, a);
+    case 1: return launch_pdl(paged_append_kernel<E5M2, 1, false>, grid, dim3(threads), 0, stream, a, reach);
+    case 2: return launch_pdl(paged_append_kernel<E5M2, 2, false>, grid, dim3(threads), 0, stream, a, reach);
+    case 4: return launch_pdl(paged_append_kernel<E5M2, 4, false>, grid, dim3(threads), 0, stream, a, reach);
+    case 8: return launch_pdl(paged_append_kernel<E5M2, 8, false>, grid, dim3(threads), 0, stream, a, reach);
     default: return cudaErrorInvalidValue;
   }
 }
