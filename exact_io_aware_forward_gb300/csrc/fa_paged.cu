@@ -34,7 +34,7 @@
 // Scales: page and head have one each.  S is multiplied by the slot's K scale
 // in float32.  V's scale goes into the weight that is multiplied with its
 // codes, w_j = 2^(s_j - m) vs_j, and the running reference m bounds
-// s_j + log2 vs_j instead of s_j, so that w lies in [0, 2] whatever the
+// s_j + ceil(log2 vs_j) instead of s_j, so that w lies in [0, 2] whatever the
 // scales are and a page of large scale costs the others no precision; the sum
 // l keeps 2^(s_j - m) in float32.
 //
@@ -69,9 +69,22 @@ constexpr float kLog2e = 1.4426950408889634f;
 // that loss.)
 constexpr float kMaxLead = 0.8f;
 constexpr float kWeightScale = 256.0f;
-// log2 of the smallest V scale that moves the reference: 2^(s - m) then
-// stays below 2^100, far from overflow.
-constexpr float kMinLogScale = -100.0f;
+// The exponent of the smallest V scale that moves the reference: 2^(s - m)
+// then stays below 2^100, far from overflow.
+constexpr int kMinScaleExponent = -100;
+
+// ceil(log2 |x|), at least kMinScaleExponent.  A whole number, so that the
+// largest slot's 2^(s - m) is a power of two and LSE loses nothing to the scale.
+__device__ __forceinline__ float scale_exponent(float x) {
+  const int bits = __float_as_int(x) & 0x7fffffff;
+  return (float)max((bits >> 23) - 127 + ((bits & 0x7fffff) != 0), kMinScaleExponent);
+}
+// m + log2(l), l > 0: the exponent of l goes to m, which it mostly cancels.
+__device__ __forceinline__ float add_log2(float m, float l) {
+  const int e = (__float_as_int(l) >> 23) - 127;
+  const bool normal = e >= -126 && e <= 126;
+  return (m + (normal ? (float)e : 0.f)) + __log2f(normal ? __int_as_float(__float_as_int(l) - (e << 23)) : l);
+}
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000u); }
 
@@ -206,6 +219,7 @@ __device__ __forceinline__ void join_terms(const float (&y)[T][8], uint64_t (&ou
 
 template <int D, int T, int G>
 struct PagedCfg {
+  static constexpr bool BF16 = T == 2;                // the 16-bit type: two terms hold a bf16, three an fp16
   static constexpr int R = 8 * G;                     // query rows of a CTA, eight a softmax group
   static constexpr int W = D == 64 ? 64 : 128;        // bytes of a shared-memory row
   static constexpr int HALVES = D == 256 ? 2 : 1;     // 128-feature parts of a K or V tile
@@ -464,7 +478,7 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
       for (int i = 0; i < E; i += 2) {
         const uint4& u = raw[i / 8];
         const uint32_t two = i % 8 == 0 ? u.x : i % 8 == 2 ? u.y : i % 8 == 4 ? u.z : u.w;
-        if (a.bf16) {
+        if (C::BF16) {
           x[i] = __uint_as_float(two << 16);
           x[i + 1] = __uint_as_float(two & 0xffff0000u);
         } else {
@@ -798,7 +812,7 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
         const int e = buf * ne + ((t * 128 + key) >> shift);
         const bool live = slot < g.len && page[(t * 128 + key) >> shift] >= 0;
         const float ks = live ? s_ks[e] : 0.f, vs = live ? s_vs[e] : 0.f;
-        const float lv = fmaxf(__log2f(fabsf(vs)), kMinLogScale), wv = vs * kWeightScale;
+        const float lv = scale_exponent(vs), wv = vs * kWeightScale;
         if (!(ok = warp_wait(&s_full[i], (j >> 1) & 1, abort_flag, a.status))) break;
         tc_fence_after();
         uint64_t s[4];
@@ -949,11 +963,13 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
       queries(k + 1);
       if (!ok) break;
       // l over the 128 slots of a tile: lanes, then warps
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[r] = f2_add(l[r], __shfl_xor_sync(0xffffffffu, l[r], o));
-        if (lane == 0) *reinterpret_cast<uint64_t*>(my_sum + quarter * 8 + 2 * r) = l[r];
+        for (int r = 0; r < 4; ++r) l[r] = f2_add(l[r], __shfl_xor_sync(0xffffffffu, l[r], o));
+      if (lane == 0) {
+        *reinterpret_cast<ulonglong2*>(my_sum + quarter * 8) = make_ulonglong2(l[0], l[1]);
+        *reinterpret_cast<ulonglong2*>(my_sum + quarter * 8 + 4) = make_ulonglong2(l[2], l[3]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&my_exchange[x & 1]);
@@ -970,15 +986,19 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
         for (int z = 0; z < 2; ++z) {
           const float y = my_sum[r + z] + my_sum[8 + r + z] + my_sum[16 + r + z] + my_sum[24 + r + z];
           v[z] = y == 0.f ? 0.f : (1.f / kWeightScale) / y;
-          if (key == r + z && r + z < rows_here) {
-            const float lse2 = y == 0.f ? neg_inf() : m[r + z] + __log2f(y);
-            if (g.part < 0)
-              a.lse[out_row + r + z] = lse2 * kLn2;
-            else
-              a.lse_part[part_row + r + z] = lse2;
-          }
         }
         inv[r / 2] = f2_pack(v[0], v[1]);
+      }
+      if (key < 8 && key < rows_here) {  // a thread a row
+        float mine = m[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r) mine = key == r ? m[r] : mine;
+        const float y = my_sum[key] + my_sum[8 + key] + my_sum[16 + key] + my_sum[24 + key];
+        const float lse2 = y == 0.f ? neg_inf() : add_log2(mine, y);
+        if (g.part < 0)
+          a.lse[out_row + key] = lse2 * kLn2;
+        else
+          a.lse_part[part_row + key] = lse2;
       }
 #pragma unroll
       for (int hf = 0; hf < C::HALVES; ++hf) {
@@ -990,20 +1010,23 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
         uint64_t o[4];
         join_terms<T>(y, o);
         const int f = hf * 128 + key;
+        float z[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          float z0, z1;
-          f2_unpack(f2_mul(o[r / 2], inv[r / 2]), z0, z1);
-          const float z = r & 1 ? z1 : z0;
-          if (r < rows_here && f < D) {
-            if (g.part >= 0) {
-              a.o_part[(part_row + r) * D + f] = z;
-            } else if (a.bf16) {
-              static_cast<__nv_bfloat16*>(a.o)[(out_row + r) * D + f] = __float2bfloat16_rn(z);
-            } else {
-              static_cast<__half*>(a.o)[(out_row + r) * D + f] = __float2half_rn(z);
-            }
-          }
+        for (int r = 0; r < 4; ++r) f2_unpack(f2_mul(o[r], inv[r]), z[2 * r], z[2 * r + 1]);
+        if (f >= D) {
+          // d = 64: the upper lanes repeat the lower ones
+        } else if (g.part >= 0) {
+          float* to = a.o_part + part_row * D + f;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < rows_here) to[r * D] = z[r];
+        } else {
+          uint16_t* to = static_cast<uint16_t*>(a.o) + out_row * D + f;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < rows_here)
+              to[r * D] = C::BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(z[r]))
+                                  : __half_as_ushort(__float2half_rn(z[r]));
         }
       }
       tc_fence_before();
