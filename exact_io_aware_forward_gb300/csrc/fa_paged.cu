@@ -217,6 +217,9 @@ __device__ __forceinline__ void join_terms(const float (&y)[T][8], uint64_t (&ou
   }
 }
 
+// CTAs on an SM for `rows` query rows a CTA.
+constexpr int paged_occupancy(int d, int rows) { return rows <= 16 && d <= 128 ? 2 : 1; }
+
 template <int D, int T, int G>
 struct PagedCfg {
   static constexpr bool BF16 = T == 2;                // the 16-bit type: two terms hold a bf16, three an fp16
@@ -229,9 +232,10 @@ struct PagedCfg {
   static constexpr uint32_t COL_O = 2 * NB;           // HALVES accumulators
   static constexpr int COLS = (2 + HALVES) * NB;
   static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  // One group: two CTAs on an SM, each with 90 KB or so of K and V in flight.
-  // More groups, or tiles of 64 KB: one CTA with all of the ring.
-  static constexpr int OCC = G == 1 && D <= 128 ? 2 : 1;
+  // One or two groups: two CTAs on an SM, which fill each other's waits (16
+  // rows of 16 x 8 heads of 8192 slots: 65 us with one, 56 with two).  More
+  // groups, or tiles of 64 KB: one CTA.
+  static constexpr int OCC = paged_occupancy(D, R);
   // Segments prepared ahead: more of them where heads may be short and their queries small.
   static constexpr int SEGS = 2;
   static constexpr int Q_BYTES = HALVES * NB * W;
@@ -1315,7 +1319,7 @@ PagedPlan paged_plan(int B, int Hkv, int rows, int d, int ps, int max_len, int n
   const int row_tiles = (rows + 39) / 40;
   p.row_tile = ((rows + row_tiles - 1) / row_tiles + 7) / 8 * 8;
   const int sms = sm_count();
-  const long long resident = (p.row_tile == 8 && d <= 128 ? 2LL : 1LL) * sms;
+  const long long resident = (long long)paged_occupancy(d, p.row_tile) * sms;
   const long long BH = (long long)B * Hkv;
   const int tiles = (max_len + 127) / 128;
   const long long all = BH * places_of(tiles);
