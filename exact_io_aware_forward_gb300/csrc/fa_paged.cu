@@ -236,8 +236,7 @@ struct PagedCfg {
   // rows of 16 x 8 heads of 8192 slots: 65 us with one, 56 with two).  More
   // groups, or tiles of 64 KB: one CTA.
   static constexpr int OCC = paged_occupancy(D, R);
-  // Segments prepared ahead: more of them where heads may be short and their queries small.
-  static constexpr int SEGS = 2;
+  static constexpr int SEGS = 2;                      // segment buffers: one in use, one being prepared
   static constexpr int Q_BYTES = HALVES * NB * W;
   static constexpr int P_BYTES = NB * 128;
   static constexpr int BUDGET = (OCC == 2 ? 104 : 192) * 1024;
@@ -262,7 +261,7 @@ struct PagedCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;             // TMEM address, abort flag
   static constexpr int OFF_DESC = (OFF_MISC + 8 + 15) / 16 * 16;  // segment descriptors of 8 ints
   static constexpr int OFF_ROW = OFF_DESC + 32 * SEGS;            // per segment: inverse scales, ends of the visible slots
-  static constexpr int OFF_MAX = OFF_ROW + 8 * SEGS * R;                // [G][2][4][8] warp maxima
+  static constexpr int OFF_MAX = OFF_ROW + 8 * SEGS * R;          // [G][2][4][8] warp maxima
   static constexpr int OFF_SUM = OFF_MAX + 32 * R;                // [G][4][8] warp sums of l
   static constexpr int OFF_PAGES = OFF_SUM + 16 * R;              // per segment and page: id, K scale, V scale
   static constexpr int WARPS = 4 * G + 4;  // a multiple of four: the SM's four parts get equally many
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
   uint64_t* s_full = ring_empty + C::NS;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
-  uint64_t* seg_pages = pv_done + 2;   // a segment's descriptor and page list are there
+  uint64_t* seg_pages = pv_done + 2;          // a segment's descriptor and page list are there
   uint64_t* seg_ready = seg_pages + C::SEGS;  // its scales and queries too
   uint64_t* seg_free = seg_ready + C::SEGS;   // all of them may be overwritten
   uint64_t* o_free = seg_free + C::SEGS;      // the accumulators have been read

@@ -594,3 +594,88 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         fa.fa_paged_append(h, new, new.half(), lens, lens.clone())
     fa.fa_device_status()
+
+
+# ---------------------------------------------------------------- large pools, streams, the example
+def test_pools_beyond_32_bits():
+    """Pages whose codes lie past 2^31 and 2^32 bytes: the same bits as from a small pool."""
+    B, Hkv, ps, d, T = 2, 8, 128, 256, 5
+    c = Cache(B, Hkv, T, ps, d, seed=300)
+    n = len(c.np[0])
+    small = c.to("cuda")
+    page = Hkv * ps * d  # bytes
+    P = (1 << 32) // page + n + 3
+    far = (torch.arange(n) * 1 + P - n).tolist()
+    far[::2] = [(1 << 31) // page + i for i in range(len(far[::2]))]  # some past 2^31, some past 2^32
+    far = torch.tensor(far)
+    k, v = (torch.empty(P, Hkv, ps, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty(P, Hkv, device="cuda") for _ in range(2))
+    for big, x in ((k, c.t[0].view(torch.uint8)), (v, c.t[1].view(torch.uint8)), (ks, c.t[2]), (vs, c.t[3])):
+        big[far.cuda()] = x
+    table = far.to(torch.int32).cuda()[c.t[4].long()].contiguous()
+    large = fa.PagedCache(k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), ks, vs, table)
+    _, q = _q(B, 16, 1, d, "bf16", 301)
+    got = []
+    for cache in (small, large):
+        lens, now = _lens([600, 577]), _lens([0, 0])
+        acc = torch.zeros(B, Hkv, T * ps, device="cuda")
+        pos = torch.zeros_like(acc, dtype=torch.int32)
+        new = torch.randn(B, Hkv, 3, d, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+        fa.fa_paged_append(cache, new, new * 2, lens, now, None, acc, pos)
+        pos.copy_(torch.arange(T * ps, device="cuda"))
+        o, lse = fa.forward_paged(cache, q.cuda(), now, weight_acc=acc)
+        ws = torch.empty(fa.fa_paged_evict_workspace_size(cache, 500), dtype=torch.uint8, device="cuda")
+        fa.fa_paged_evict(cache, now, lens, acc, pos, ws, 500, 50)
+        o2, lse2 = fa.forward_paged(cache, q.cuda(), lens)
+        fa.fa_device_status()
+        got.append((o, lse, acc, pos, lens, o2, lse2))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    for big, x in ((k, c.t[0].view(torch.uint8)), (ks, c.t[2])):
+        assert torch.equal(big[far.cuda()], x)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with its own workspace, on streams other than the tensors' own."""
+    runs = []
+    for i, (B, Hq, Hkv, Nq, d, n) in enumerate([(3, 8, 2, 1, 128, 9000), (2, 16, 2, 4, 256, 5000), (4, 4, 4, 1, 64, 7000)]):
+        c = Cache(B, Hkv, (n + 63) // 64, 64, d, seed=310 + i)
+        _, q = _q(B, Hq, Nq, d, "bf16", 320 + i)
+        runs.append((c.to("cuda"), q.cuda(), _lens([n, n - 777, 5, 300][:B]), c))
+    alone = [fa.forward_paged(h, q, lens, causal=True) for h, q, lens, _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        streams = [torch.cuda.Stream() for _ in runs]
+        got = [fa.forward_paged(h, q, lens, causal=True, stream=s) for (h, q, lens, _), s in zip(runs, streams)]
+        for s in streams:
+            s.synchronize()
+        fa.fa_device_status()
+        assert all(torch.equal(x, y) for a, b in zip(alone, got) for x, y in zip(a, b))
+    o, lse = fa.forward_paged(*runs[0][:3], causal=True, stream=streams[0].cuda_stream)  # a raw handle
+    streams[0].synchronize()
+    assert torch.equal(o, alone[0][0])
+
+
+def test_the_loop_of_the_documentation():
+    P, Hkv, ps, d, B, T = 128, 8, 64, 128, 4, 16
+    k, v = (torch.zeros(P, Hkv, ps, d, device="cuda", dtype=torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.zeros(P, Hkv, device="cuda") for _ in range(2))
+    table = torch.randperm(P, device="cuda")[:B * T].view(B, T).int()
+    cache = fa.PagedCache(k, v, ks, vs, table)
+    lens, now = (torch.zeros(B, device="cuda", dtype=torch.int32) for _ in range(2))
+    weight = torch.zeros(B, Hkv, cache.slots, device="cuda")
+    pos, first = torch.zeros_like(weight, dtype=torch.int32), torch.zeros_like(lens)
+    ws = torch.empty(fa.fa_paged_evict_workspace_size(cache, 512), device="cuda", dtype=torch.uint8)
+    for N in (500, 1, 30, 1, 1):
+        k_new, v_new = (torch.randn(B, Hkv, N, d, device="cuda").bfloat16() for _ in range(2))
+        q = torch.randn(B, 32, N if N > 1 else 1, d, device="cuda").bfloat16()
+        fa.fa_paged_append(cache, k_new, v_new, lens, now, weight_acc=weight, positions=pos, first_position=first)
+        o, lse = fa.forward_paged(cache, q, now, causal=True, weight_acc=weight)
+        fa.fa_paged_evict(cache, now, lens, weight, pos, ws, keep=512, recent=256)
+        first += N
+        fa.fa_device_status()
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert lens.tolist() == [512] * B and first.tolist() == [533] * B
+    # the last 256 tokens are all there, in every head
+    for b in range(B):
+        for h in range(Hkv):
+            assert set(range(533 - 256, 533)) <= set(pos[b, h, :512].tolist())
