@@ -86,7 +86,7 @@ fa_status attention_plan(const fa_paged_cache* c, int Hq, int Nq, int max_len, i
   p->score_rows = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
   p->score_groups = (int)((rows + 7) / 8);
   p->score_stride = (long long)p->max_len * p->score_rows;
-  if (weights) p->scores = align256((size_t)BH * p->score_groups * p->score_stride * sizeof(float) );
+  if (weights) p->scores = align256((size_t)BH * p->score_groups * p->score_stride * sizeof(float));
   return FA_OK;
 }
 

@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
   }
   int above = (int)shielded, in = n - above;  // keys over the window, and in it
   if (above >= m) lo = hi = 0xffffffffu, in = above, above = 0;
-  for (int pass = 0; in != m - above && lo != hi; ++pass) {
+  // each pass leaves at most 2^shift keys' width, shift <= 24, 16, 8, 0: four are enough
+  for (int pass = 0; pass < 4 && in != m - above && lo != hi; ++pass) {
     const int turn = pass & 1;
     const int shift = max(0, 24 - __clz(hi - lo));  // at most 256 bins
     int* bin = s_bin[turn];
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(TH) paged_select_kernel(const __grid_constant_
     }
     __syncthreads();
     lo += (uint32_t)s_pick[turn][0] << shift;
-    hi = min(hi, lo + ((1u << shift) - 1u));
+    hi = lo + min(hi - lo, (1u << shift) - 1u);  // lo + 2^shift may pass 2^32 (NaN's key is near it)
     above += s_pick[turn][1];
     in = s_pick[turn][2];
   }

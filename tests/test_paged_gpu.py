@@ -448,6 +448,28 @@ def test_evict_long_heads(n, ps, kind):
     assert all(np.array_equal(x, y) for x, y in zip(got, want))
 
 
+@pytest.mark.parametrize("kind", ["nan", "inf", "huge"])
+@pytest.mark.parametrize("n,ps", [(600, 64), (30000, 128)])
+def test_evict_many_of_the_largest(kind, n, ps):
+    """More slots than stay with NaN, infinite or very large weights over small, and over negative, others."""
+    rng = np.random.default_rng(77)
+    T = (n + ps - 1) // ps
+    for low in (1e-38, 1e-3, -1e-3, -1e30, -3e38):
+        c = Cache(1, 2, T, ps, 64, seed=76)
+        w = (rng.random((1, 2, T * ps)) * low).astype(np.float32)
+        top = rng.random(w.shape) < 0.6
+        w[top] = {"nan": np.nan, "inf": np.inf, "huge": 1.0}[kind]
+        if kind == "huge":
+            w[top] = 3e38 * rng.random(int(top.sum()))
+        pos = np.broadcast_to(np.arange(T * ps, dtype=np.int32), w.shape).copy()
+        for keep in (n // 2 - 3, n // 5) if n < 1000 else (n // 50,):
+            acc, position, new_lens = _run_evict(c, w, pos, [n], keep, 9)
+            fa.fa_device_status()
+            want = P.evict(c.np, "e4m3", c.table, w, pos, np.array([n]), keep, 9)
+            got = c.read() + [acc.cpu().numpy(), position.cpu().numpy(), new_lens.cpu().numpy()]
+            assert all(np.array_equal(x, y, equal_nan=x.dtype.kind == "f") for x, y in zip(got, want)), (low, keep)
+
+
 def test_evict_when_all_weights_are_equal():
     for value in (0.0, -0.0, np.inf, np.nan, -3.0):
         c = Cache(2, 1, 10, 64, 64, seed=72)
