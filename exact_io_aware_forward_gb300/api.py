@@ -524,6 +524,13 @@ class PagedCache:
         return None if t is None else self._tensor(name, t, (self.B, self.Hkv, self.slots), dtype)
 
 
+def _int32(name, x):
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 def _workspace_args(cache, workspace):
     if workspace.dtype != torch.uint8 or workspace.device != cache.device or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 tensor on the cache's device")
@@ -550,8 +557,8 @@ def fa_paged_append(cache, k, v, lens, new_lens, counts=None, weight_acc=None, p
 
 
 def fa_paged_workspace_size(cache, Hq, Nq, max_len=0, num_splits=0, weights=False) -> int:
-    return int(lib().fa_paged_workspace_size(cache._ref, int(Hq), int(Nq), int(max_len), int(num_splits),
-                                             int(bool(weights))))
+    return int(lib().fa_paged_workspace_size(cache._ref, _int32("Hq", Hq), _int32("Nq", Nq), _int32("max_len", max_len),
+                                             _int32("num_splits", num_splits), int(bool(weights))))
 
 
 def fa_forward_paged(cache, q, lens, o, lse, workspace, causal=False, scale=None, weight_acc=None, max_len=0,
@@ -569,11 +576,12 @@ def fa_forward_paged(cache, q, lens, o, lse, workspace, causal=False, scale=None
         cache._ref, cache._tensor("q", q, shape, dt), cache._tensor("lens", lens, (cache.B,), torch.int32),
         cache._tensor("o", o, shape, dt), cache._tensor("lse", lse, shape[:3], torch.float32),
         cache._state("weight_acc", weight_acc, torch.float32), Hq, Nq, _DTYPE_CODE[dt], int(bool(causal)),
-        _scale(scale, d), int(max_len), int(num_splits), ws, ws_bytes, cache._stream(stream)))
+        _scale(scale, d), _int32("max_len", max_len), _int32("num_splits", num_splits), ws, ws_bytes,
+        cache._stream(stream)))
 
 
 def fa_paged_evict_workspace_size(cache, keep) -> int:
-    return int(lib().fa_paged_evict_workspace_size(cache._ref, int(keep)))
+    return int(lib().fa_paged_evict_workspace_size(cache._ref, _int32("keep", keep)))
 
 
 def fa_paged_evict(cache, lens, new_lens, weight_acc, positions, workspace, keep, recent, stream=None) -> None:
@@ -587,7 +595,7 @@ def fa_paged_evict(cache, lens, new_lens, weight_acc, positions, workspace, keep
     _check("fa_paged_evict", lib().fa_paged_evict(
         cache._ref, cache._tensor("lens", lens, B, torch.int32), cache._tensor("new_lens", new_lens, B, torch.int32),
         cache._state("weight_acc", weight_acc, torch.float32), cache._state("positions", positions, torch.int32),
-        int(keep), int(recent), ws, ws_bytes, cache._stream(stream)))
+        _int32("keep", keep), _int32("recent", recent), ws, ws_bytes, cache._stream(stream)))
 
 
 def fa_selftest_wait_timeout(stream=None) -> None:

@@ -539,8 +539,10 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
         if (!a.balanced || at >= stop) return;
         if (++h == a.c.Hkv) {
           h = 0;
-          do tb = tiles_of(++b);
-          while (tb == 0);
+          do {
+            if (++b >= a.c.B) return;  // only if the lengths change while they are read
+            tb = tiles_of(b);
+          } while (tb == 0);
         }
         place(at);
       } while (n <= 0);
@@ -769,8 +771,8 @@ __global__ void __launch_bounds__(PagedCfg<D, T, G>::WARPS * 32, (PagedCfg<D, T,
     // byte of this slot in row 0 of the group's weights; row r is at 128 r with
     // the 16-byte chunk XORed with r (the buffer begins on a 1024-byte boundary)
     const uint32_t p_byte = smem_u32(sP) + g8 * 128 + key;
-    // far below all scores, so that -inf - m is -inf
-    constexpr float kNothing = -1e30f;
+    // the lowest number: no score but -inf is below it, and -inf - m is -inf
+    constexpr float kNothing = -3.402823466e38f;
     int j = 0;  // tile over all segments
     int x = 0;  // exchanges so far
     bool ok = true;

@@ -158,7 +158,7 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const void* q, const int
   AttnPlan p;
   if ((st = attention_plan(cache, Hq, Nq, max_len, num_splits, weight_acc != nullptr, &p)) != FA_OK) return st;
   if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
-  if (!(isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (!(isfinite(scale * kLog2e) && scale > 0.f)) return FA_ERR_INVALID_ARG;
   fa::PagedAttnArgs a;
   if ((st = view(cache, &a.c)) != FA_OK) return st;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(lens) || (weight_acc && !aligned16(weight_acc)))

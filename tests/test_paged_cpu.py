@@ -66,7 +66,7 @@ def test_null_cache(lib):
     (dict(q=None), INVALID), (dict(q=PTR + 2), INVALID), (dict(lens=None), INVALID), (dict(lens=PTR + 2), INVALID),
     (dict(o=PTR + 8), INVALID), (dict(lse=None), INVALID), (dict(acc=PTR + 4), INVALID), (dict(Hq=6), INVALID),
     (dict(Hq=0), INVALID), (dict(Nq=0), INVALID), (dict(dt=2), UNSUPPORTED), (dict(scale=0.0), INVALID),
-    (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID), (dict(max_len=513), INVALID),
+    (dict(scale=3e38), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID), (dict(max_len=513), INVALID),
     (dict(max_len=-1), INVALID), (dict(splits=-1), INVALID), (dict(splits=1025), INVALID), (dict(ws=None), WORKSPACE),
     (dict(ws=PTR + 16), WORKSPACE), (dict(splits=4, ws_bytes=100), WORKSPACE), (dict(acc=PTR, ws_bytes=100), WORKSPACE),
     (dict(Nq=1 << 22), UNSUPPORTED)])

@@ -217,6 +217,35 @@ def test_not_finite_queries_stay_in_their_row():
         assert np.abs(lse.cpu().double().numpy() - rl)[good].max() < 1e-3
 
 
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_scores_far_below_zero(splits):
+    """Scores of about -1e33 to -1e37: all keys equal, and one slot's score half of the others'.
+
+    Equal scores: every weight is a power of two (the V scales are), O is V's mean; its 700 terms are rounded in 32-bit
+    sums (2^-23 each, 2^-13 of the largest |V|), and once to bf16, 2^-8.  LSE: seven roundings of 2^-24 (log2 e, scale
+    and their product, times the page's scale, times the row's, ln 2, the result); ln 700 is far below one of them, so
+    that parts of a row joined by their LSE weigh alike whatever they hold: that O is looked at where there is one."""
+    n, d = 700, 64
+    c = Cache(2, 1, 11, 64, d, "e4m3", seed=90, powers=True)
+    c.np[0][:] = P.encode(np.array([1.0]), "e4m3")[0]
+    c.np[3][:] = 0.25
+    c.np[0][c.table[1, 7], 0, 13] = P.encode(np.array([0.5]), "e4m3")[0]
+    q = torch.full((2, 2, 1, d), -1.0).bfloat16()
+    q[:, 1] = -1000.0
+    for ks in (1e32, 1e34):
+        c.np[2][:] = np.float32(ks)
+        o, lse = fa.forward_paged(c.to("cuda"), q.cuda(), _lens([n, n]), scale=0.125, num_splits=splits)
+        fa.fa_device_status()
+        ro, rl, _, _ = P.attention(q.double().numpy(), c.np, "e4m3", c.table, [n, n], 0.125, False)
+        o, lse = o.cpu().double().numpy(), lse.cpu().double().numpy()
+        assert np.isfinite(rl).all() and rl.max() < -1e32
+        assert (np.abs(lse - rl) <= 7 * 2.0 ** -24 * np.abs(rl)).all()
+        if splits == 1:
+            assert (np.abs(o - ro)[0] <= 2.0 ** -13 * 448 * 0.25 + 2.0 ** -8 * np.abs(ro[0])).all()
+        one = P.code_values("e4m3")[c.np[1][c.table[1, 7], 0, 13]] * 0.25  # the one slot's V, all of O
+        assert np.array_equal(o[1, 0, 0], one) and np.array_equal(o[1, 1, 0], one)
+
+
 def test_zero_and_tiny_rows():
     """A query of zeros, one of subnormal numbers, pages of zeros with the smallest scale."""
     c = Cache(1, 1, 3, 64, 64, seed=13)
@@ -610,6 +639,16 @@ def test_python_refusals():
         fa.forward_paged(h, q, lens, weight_acc=torch.zeros(2, 2, 64, device="cuda"))
     with pytest.raises(fa.FAError):
         fa.forward_paged(h, q[:, :3].contiguous(), lens)
+    for kw in (dict(max_len=1 << 32), dict(num_splits=(1 << 32) + 1)):
+        with pytest.raises(ValueError):
+            fa.forward_paged(h, q, lens, **kw)
+    with pytest.raises(ValueError):
+        fa.fa_paged_evict_workspace_size(h, (1 << 32) + 5)
+    acc, pos = torch.zeros(2, 2, 128, device="cuda"), torch.zeros(2, 2, 128, device="cuda", dtype=torch.int32)
+    ws = torch.empty(1 << 20, device="cuda", dtype=torch.uint8)
+    for keep, recent in (((1 << 32) + 5, 1), (5, 1 << 32)):
+        with pytest.raises(ValueError):
+            fa.fa_paged_evict(h, lens, lens.clone(), acc, pos, ws, keep, recent)
     new = torch.zeros(2, 2, 1, 64, device="cuda", dtype=torch.bfloat16)
     with pytest.raises(fa.FAError):
         fa.fa_paged_append(h, new, new, lens, lens)
